@@ -500,6 +500,66 @@ moe_status moe_reduce_fused_scaled(const void* expert_out, int64_t rows,
                                    const float* x_sf, const float* sf, int T, int K, int H,
                                    int in_dtype, int out_dtype, void* y, void* stream);
 
+/* The norms around a block: the norm of a block's output, its gate and
+ * residual scale, the residual sum, and the norm in front of the next block
+ * (with that block's activation quantiser), in one pass. Per token t, with
+ * rstd(u) = 1 / sqrt(mean(u^2) + eps) over the H values of a row:
+ *   b = y[t] * rstd(y[t]) * gamma_post      (y[t] itself if gamma_post is NULL)
+ *   r = residual[t] + (alpha * gate) * b
+ *   n = r * rstd(r) * gamma_pre
+ *   residual_out[t] = R(r),  h[t] = R(n),  (codes, scales)[t] = Q(n)
+ * in fp32; each output is rounded once, from the unrounded r and n.
+ *   y            [T, H] of dtype, or NULL: r = residual (the norm in front of
+ *                the first block); then gamma_post, gate and residual_out are
+ *                NULL.
+ *   residual     [T, H] of res_dtype: dtype, or MOE_F32 (an fp32 residual
+ *                stream next to 16-bit activations).
+ *   gamma_post, gamma_pre   fp32 [H]; gamma_pre NULL: no h, codes and scales.
+ *   gate         by gate_kind: NULL (MOE_GATE_NONE), fp32 [H] (_CHANNEL),
+ *                fp32 [T] (_TOKEN) or dtype [T, H] (_FULL).
+ *   residual_out [T, H] of res_dtype, or NULL; may be `residual` itself.
+ *   h            [T, H] of dtype, or NULL; may be `y` itself.
+ *   quant        MOE_QUANT_NONE, or the form of the quantised experts'
+ *                activations: _FP8 (E4M3 codes [T, H], fp32 scales [T] =
+ *                row amax / 448), _INT8 (int8 codes [T, H], fp32 scales [T] =
+ *                row amax / 127; both 1 for a zero row), _MXFP8 / _MXFP4
+ *                (codes [T, H] / [T, H/2], E8M0 scales [T, H/32]); the
+ *                definitions of moe_quantize_fp8_rows, _int8_rows and _mx_rows
+ *                with n in fp32 (not rounded to dtype first).
+ * dtype: MOE_F16, MOE_BF16 or MOE_F32. Requires T >= 0, 1 <= H <= 16384,
+ * eps > 0; the MX forms need H % 32 == 0 and y, residual, residual_out, h,
+ * codes, the gammas and the gate on 16-byte boundaries. Other buffers must
+ * not overlap. Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE,
+ * MOE_ERR_UNSUPPORTED (gate_kind, quant), MOE_ERR_HIP. */
+#define MOE_GATE_NONE 0
+#define MOE_GATE_CHANNEL 1
+#define MOE_GATE_TOKEN 2
+#define MOE_GATE_FULL 3
+#define MOE_QUANT_NONE 0
+#define MOE_QUANT_FP8 1
+#define MOE_QUANT_INT8 2
+#define MOE_QUANT_MXFP8 3
+#define MOE_QUANT_MXFP4 4
+#define MOE_NORM_MAX_H 16384
+moe_status moe_block_norm(const void* y, const void* residual, const float* gamma_post,
+                          const void* gate, int gate_kind, float alpha, const float* gamma_pre,
+                          float eps, int T, int H, int dtype, int res_dtype, void* residual_out,
+                          void* h, int quant, void* codes, void* scales, void* stream);
+
+/* Step 3 with the norms in its epilogue: moe_block_norm of
+ *   y[t] = sum over k ascending with pos[t,k] >= 0 of
+ *          w[t,k] * expert_out[pos[t,k]]
+ * (the sum of moe_reduce_fused, kept in fp32 and never stored). expert_out
+ * [rows, H] of dtype, token_topk_to_pos and topk_weights as moe_reduce_fused
+ * takes them; the rest as moe_block_norm (a token whose slots are all masked
+ * has y = 0). Requires H % 256 == 0 and 1 <= K <= 64 as well. */
+moe_status moe_reduce_norm(const void* expert_out, int64_t rows,
+                           const int32_t* token_topk_to_pos, const float* topk_weights, int K,
+                           const void* residual, const float* gamma_post, const void* gate,
+                           int gate_kind, float alpha, const float* gamma_pre, float eps, int T,
+                           int H, int dtype, int res_dtype, void* residual_out, void* h, int quant,
+                           void* codes, void* scales, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

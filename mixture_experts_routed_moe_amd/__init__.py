@@ -10,15 +10,16 @@ MoeError with the library's status code on any failure.
     tables = moe_dispatch(topk_ids, topk_weights, num_experts)      # step 1
     y = moe_routed_forward(x, w_gate, w_up, w_down, tables)         # steps 2-3
     y = moe_reduce_fused(expert_out, token_topk_to_pos, topk_weights)  # step 3 alone
+    residual, h = moe_block_norm(y, residual, gamma_post, gamma_pre)   # the norms between blocks
 """
+import contextlib
 import ctypes
 import math
 
 import torch
 
-from ._lib import (MOE_BF16, MOE_ERR_DTYPE, MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_F16, MOE_F32,
-                   MOE_FP8_E4M3,
-                   MoeError, MoeTablesStruct, check, lib)
+from ._lib import (MOE_BF16, MOE_ERR_DTYPE, MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED,
+                   MOE_F16, MOE_F32, MOE_FP8_E4M3, MoeError, MoeTablesStruct, check, lib)
 
 __all__ = ["MoeError", "MoeTables", "FP8Weights", "default_block_m", "moe_gate", "moe_dispatch",
            "quantize_fp8_rows", "moe_expert_gate_up_w8", "moe_expert_down_w8",
@@ -29,7 +30,7 @@ __all__ = ["MoeError", "MoeTables", "FP8Weights", "default_block_m", "moe_gate",
            "moe_expert_gate_up_w4a8", "moe_expert_down_w4a8", "forward_w4a8_workspace",
            "moe_routed_forward_w4a8", "MX_FP8", "MX_FP4", "MXWeights", "quantize_mx_rows",
            "quantize_mx_weights", "moe_expert_gate_up_mx", "moe_expert_down_mx",
-           "forward_mx_workspace", "moe_routed_forward_mx"]
+           "forward_mx_workspace", "moe_routed_forward_mx", "moe_block_norm", "moe_reduce_norm"]
 
 MX_FP8, MX_FP4 = 0, 4
 
@@ -937,3 +938,145 @@ def moe_reduce_fused(expert_out, token_topk_to_pos, topk_weights=None, out_dtype
                                             _REDUCE_CODE[expert_out.dtype],
                                             _REDUCE_CODE[out_dtype], _ptr(y), _stream(dev)))
     return y
+
+
+_NO_GUARD = contextlib.nullcontext()
+
+
+def _on(device):
+    """The device of the operands as the current one (a launch goes to the current device)."""
+    return _NO_GUARD if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+_GATE_NONE, _GATE_CHANNEL, _GATE_TOKEN, _GATE_FULL = 0, 1, 2, 3
+# quant= of the norm calls: MOE_QUANT_* code, dtype of the codes
+_NORM_QUANT = {"fp8": (1, torch.uint8), "int8": (2, torch.int8), "mxfp8": (3, torch.uint8),
+               "mxfp4": (4, torch.uint8)}
+
+
+def _norm_gate(gate, T, H, dtype, device):
+    """(MOE_GATE_* code) of a gate: float32 [H], float32 [T, 1] or dtype [T, H]."""
+    if gate is None:
+        return _GATE_NONE
+    _check_tensor(gate, "gate", None, None, device)
+    shape = tuple(gate.shape)
+    if shape == (H,) and gate.dtype == torch.float32:
+        return _GATE_CHANNEL
+    if shape == (T, 1) and gate.dtype == torch.float32:
+        return _GATE_TOKEN
+    _require(shape in ((H,), (T, 1), (T, H)), MOE_ERR_SHAPE,
+             "gate must be [%d], [%d, 1] or [%d, %d] (got %s)" % (H, T, T, H, shape))
+    _require(shape == (T, H) and gate.dtype == dtype, MOE_ERR_DTYPE,
+             "gate must be float32 [H], float32 [T, 1] or %s [T, H] (got %s)" % (dtype, gate.dtype))
+    return _GATE_FULL
+
+
+def _run_norm(fn, head, dtype, T, H, residual, gamma_post, gamma_pre, gate, alpha, eps, quant,
+              residual_out, h, codes, scales, has_y):
+    """Checks and call shared by moe_block_norm and moe_reduce_norm; `head` are the
+    arguments in front of `residual`."""
+    dev = residual.device
+    _require(dtype in _DTYPE_CODE, MOE_ERR_DTYPE, "activations must be float16, bfloat16 or float32")
+    _require(residual.dtype in (dtype, torch.float32), MOE_ERR_DTYPE,
+             "residual must be %s or float32 (got %s)" % (dtype, residual.dtype))
+    for n, g in (("gamma_post", gamma_post), ("gamma_pre", gamma_pre)):
+        if g is not None:
+            _check_tensor(g, n, torch.float32, 1, dev)
+            _require(g.shape[0] == H, MOE_ERR_SHAPE, "%s must be [%d]" % (n, H))
+    kind = _norm_gate(gate, T, H, dtype, dev)
+    _require(quant is None or quant in _NORM_QUANT, MOE_ERR_UNSUPPORTED,
+             "quant must be None or one of %s (got %r)" % (", ".join(sorted(_NORM_QUANT)), quant))
+    if has_y:
+        if residual_out is None:
+            residual_out = torch.empty_like(residual)
+        _check_tensor(residual_out, "residual_out", residual.dtype, 2, dev)
+        _require(tuple(residual_out.shape) == (T, H), MOE_ERR_SHAPE, "residual_out must be [T, H]")
+    else:
+        _require(residual_out is None, MOE_ERR_NULL, "without y there is no residual_out")
+    qcode = 0
+    if gamma_pre is not None:
+        if h is None:
+            h = torch.empty((T, H), dtype=dtype, device=dev)
+        _check_tensor(h, "h", dtype, 2, dev)
+        _require(tuple(h.shape) == (T, H), MOE_ERR_SHAPE, "h must be [T, H]")
+    else:
+        _require(h is None and quant is None, MOE_ERR_NULL, "h and codes need gamma_pre")
+    if quant is not None:
+        qcode, ctype = _NORM_QUANT[quant]
+        mx = quant.startswith("mx")
+        cshape = (T, H // 2) if quant == "mxfp4" else (T, H)
+        sshape, stype = ((T, H // 32), torch.uint8) if mx else ((T,), torch.float32)
+        if codes is None:
+            codes = torch.empty(cshape, dtype=ctype, device=dev)
+        if scales is None:
+            scales = torch.empty(sshape, dtype=stype, device=dev)
+        _check_tensor(codes, "codes", ctype, 2, dev)
+        _check_tensor(scales, "scales", stype, len(sshape), dev)
+        _require(tuple(codes.shape) == cshape and tuple(scales.shape) == sshape, MOE_ERR_SHAPE,
+                 "codes must be %s and scales %s" % (cshape, sshape))
+    else:
+        _require(codes is None and scales is None, MOE_ERR_NULL, "codes and scales need a quant")
+    if T == 0:
+        return (residual_out, h) if quant is None else (residual_out, h, codes, scales)
+    with _on(dev):
+        check(fn(*head, _address(residual), _address(gamma_post), _address(gate), kind, alpha,
+                 _address(gamma_pre), eps, T, H, _DTYPE_CODE[dtype], _DTYPE_CODE[residual.dtype],
+                 _address(residual_out), _address(h), qcode, _address(codes), _address(scales),
+                 _stream(dev)))
+    return (residual_out, h) if quant is None else (residual_out, h, codes, scales)
+
+
+def moe_block_norm(y, residual, gamma_post=None, gamma_pre=None, gate=None, alpha=1.0, eps=1e-6,
+                   quant=None, residual_out=None, h=None, codes=None, scales=None, dtype=None):
+    """The norms around a block in one pass: with N(v) = v / sqrt(mean v^2 + eps) * gamma,
+    r = residual + (alpha * gate) * N_post(y) and h = N_pre(r), in fp32.
+
+    y [T, H] float16 / bfloat16 / float32, or None (the norm in front of the
+    first block: r = residual, `dtype` of h defaults to residual's);
+    residual [T, H] of y's dtype or float32; gamma_post / gamma_pre float32 [H]
+    (gamma_post None: y is added unnormalised; gamma_pre None: no h); gate
+    float32 [H], float32 [T, 1] or [T, H] of y's dtype; quant None, "fp8",
+    "int8", "mxfp8" or "mxfp4" (h as the quantised experts take it, quantised
+    from fp32). residual_out may be `residual` and h may be `y`.
+    Returns (residual_out, h), with quant (residual_out, h, codes, scales);
+    what is not asked for is None."""
+    _check_tensor(residual, "residual", None, 2)
+    T, H = residual.shape
+    if y is not None:
+        _check_tensor(y, "y", None, 2, residual.device)
+        _require(tuple(y.shape) == (T, H), MOE_ERR_SHAPE, "y must be [T, H] = %s" % ((T, H),))
+        _require(dtype is None or dtype == y.dtype, MOE_ERR_DTYPE, "dtype is y's")
+        dtype = y.dtype
+    elif dtype is None:
+        dtype = residual.dtype
+    return _run_norm(lib().moe_block_norm, (_address(y),), dtype, T, H, residual, gamma_post,
+                     gamma_pre, gate, alpha, eps, quant, residual_out, h, codes, scales, y is not None)
+
+
+def moe_reduce_norm(expert_out, token_topk_to_pos, topk_weights, residual, gamma_post=None,
+                    gamma_pre=None, gate=None, alpha=1.0, eps=1e-6, quant=None, residual_out=None,
+                    h=None, codes=None, scales=None):
+    """Step 3 with the norms around the block in its epilogue: moe_block_norm of
+    y[t] = sum_k w[t,k] * expert_out[pos[t,k]] over pos >= 0, which stays in
+    fp32 and is never stored. expert_out [rows, H] (H a multiple of 256),
+    token_topk_to_pos int32 [T, K], topk_weights float32 [T, K] or None; the
+    rest and the result as moe_block_norm."""
+    _check_tensor(residual, "residual", None, 2)
+    T, H = residual.shape
+    dev = residual.device
+    _check_tensor(expert_out, "expert_out", None, 2, dev)
+    _require(expert_out.shape[1] == H, MOE_ERR_SHAPE, "expert_out must be [rows, %d]" % H)
+    _check_tensor(token_topk_to_pos, "token_topk_to_pos", torch.int32, 2, dev)
+    _require(token_topk_to_pos.shape[0] == T, MOE_ERR_SHAPE, "token_topk_to_pos must be [%d, K]" % T)
+    K = token_topk_to_pos.shape[1]
+    if topk_weights is not None:
+        _check_tensor(topk_weights, "topk_weights", torch.float32, 2, dev)
+        _require(tuple(topk_weights.shape) == (T, K), MOE_ERR_SHAPE, "topk_weights must be [%d, %d]" % (T, K))
+    head = (_address(expert_out), expert_out.shape[0], _address(token_topk_to_pos),
+            _address(topk_weights), K)
+    return _run_norm(lib().moe_reduce_norm, head, expert_out.dtype, T, H, residual, gamma_post,
+                     gamma_pre, gate, alpha, eps, quant, residual_out, h, codes, scales, True)

@@ -135,6 +135,12 @@ def lib():
         L.moe_routed_forward_mx.argtypes = [vp, vp, vp, vp, vp, vp, vp, tp, i32, i32, i32, vp, sz,
                                             vp, vp]
         L.moe_routed_forward_mx.restype = i32
+        f32 = ctypes.c_float
+        norm = [vp, vp, vp, i32, f32, vp, f32, i32, i32, i32, i32, vp, vp, i32, vp, vp, vp]
+        L.moe_block_norm.argtypes = [vp] + norm
+        L.moe_block_norm.restype = i32
+        L.moe_reduce_norm.argtypes = [vp, i64, vp, vp, i32] + norm
+        L.moe_reduce_norm.restype = i32
         _lib = L
     return _lib
 

@@ -6,6 +6,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstdint>
+#include <initializer_list>
 #include <string>
 
 #include "launch.hpp"
@@ -859,6 +860,84 @@ moe_status moe_reduce_fused(const void* expert_out, int64_t rows,
                             int K, int H, int in_dtype, int out_dtype, void* y, void* stream) {
   return moe_reduce_fused_scaled(expert_out, rows, token_topk_to_pos, topk_weights, nullptr,
                                  nullptr, T, K, H, in_dtype, out_dtype, y, stream);
+}
+
+// Checks of the two norm calls that do not depend on where y comes from, and
+// the launch. p.y, p.pos, p.w, p.rows and p.K are set by the caller.
+static moe_status run_norm(moe::NormProblem& p, hipStream_t stream, const char* what) {
+  if (!p.res) return fail(MOE_ERR_NULL, "residual must not be NULL");
+  if (p.gate_kind < MOE_GATE_NONE || p.gate_kind > MOE_GATE_FULL) {
+    return fail(MOE_ERR_UNSUPPORTED, "gate_kind %d is not one of MOE_GATE_*", p.gate_kind);
+  }
+  if (p.quant < MOE_QUANT_NONE || p.quant > MOE_QUANT_MXFP4) {
+    return fail(MOE_ERR_UNSUPPORTED, "quant %d is not one of MOE_QUANT_*", p.quant);
+  }
+  if ((p.gate_kind != MOE_GATE_NONE) != (p.gate != nullptr)) {
+    return fail(MOE_ERR_NULL, "gate must be given with a gate_kind, and only then");
+  }
+  if (!p.y && (p.gamma_post || p.gate || p.res_out)) {
+    return fail(MOE_ERR_NULL, "without y there is no gamma_post, gate or residual_out");
+  }
+  if ((p.quant != MOE_QUANT_NONE) != (p.codes != nullptr) || !p.codes != !p.scales) {
+    return fail(MOE_ERR_NULL, "codes and scales must be given with a quant, and only then");
+  }
+  if (!p.gamma_pre && (p.h || p.codes)) return fail(MOE_ERR_NULL, "h and codes need gamma_pre");
+  if (!p.res_out && !p.h && !p.codes) {
+    return fail(MOE_ERR_NULL, "one of residual_out, h and codes must not be NULL");
+  }
+  if (!p.h && !p.codes) p.gamma_pre = nullptr;   // nothing to norm for
+  if (p.T < 0) return fail(MOE_ERR_SHAPE, "T must be >= 0 (got %d)", p.T);
+  if (p.H < 1 || p.H > MOE_NORM_MAX_H) {
+    return fail(MOE_ERR_SHAPE, "H must be in [1, %d] (got %d)", MOE_NORM_MAX_H, p.H);
+  }
+  if (!(p.eps > 0.0f)) return fail(MOE_ERR_SHAPE, "eps must be > 0 (got %g)", p.eps);
+  if (!is_float(p.dtype)) return fail(MOE_ERR_DTYPE, "dtype must be MOE_F16, MOE_BF16 or MOE_F32");
+  if (p.res_dtype != p.dtype && p.res_dtype != MOE_F32) {
+    return fail(MOE_ERR_DTYPE, "res_dtype must be dtype or MOE_F32");
+  }
+  if (p.T > (1 << 22) - 1) return fail(MOE_ERR_SHAPE, "T too large for one launch (got %d)", p.T);
+  uintptr_t bits = 0;
+  for (const void* q : {p.y, p.res, static_cast<const void*>(p.gamma_post), p.gate,
+                        static_cast<const void*>(p.gamma_pre), static_cast<const void*>(p.res_out),
+                        static_cast<const void*>(p.h), static_cast<const void*>(p.codes)}) {
+    if (q != p.gate || p.gate_kind != MOE_GATE_TOKEN) bits |= reinterpret_cast<uintptr_t>(q);
+  }
+  p.vec = p.H % 8 == 0 && bits % 16 == 0;
+  if ((p.quant == MOE_QUANT_MXFP8 || p.quant == MOE_QUANT_MXFP4) && (p.H % 32 != 0 || !p.vec)) {
+    return fail(MOE_ERR_SHAPE, "the MX forms need H %% 32 == 0 (got %d) and 16-byte aligned arrays", p.H);
+  }
+  if (p.T == 0) return ok();
+  return hip_status(moe::launch_block_norm(p, stream), what);
+}
+
+moe_status moe_block_norm(const void* y, const void* residual, const float* gamma_post,
+                          const void* gate, int gate_kind, float alpha, const float* gamma_pre,
+                          float eps, int T, int H, int dtype, int res_dtype, void* residual_out,
+                          void* h, int quant, void* codes, void* scales, void* stream) {
+  moe::NormProblem p{y, 0, nullptr, nullptr, 0, residual, gamma_post, gate, gate_kind, alpha,
+                     gamma_pre, eps, T, H, dtype, res_dtype, residual_out, h, quant, codes, scales,
+                     false};
+  return run_norm(p, static_cast<hipStream_t>(stream), "moe_block_norm launch");
+}
+
+moe_status moe_reduce_norm(const void* expert_out, int64_t rows,
+                           const int32_t* token_topk_to_pos, const float* topk_weights, int K,
+                           const void* residual, const float* gamma_post, const void* gate,
+                           int gate_kind, float alpha, const float* gamma_pre, float eps, int T,
+                           int H, int dtype, int res_dtype, void* residual_out, void* h, int quant,
+                           void* codes, void* scales, void* stream) {
+  if (!expert_out || !token_topk_to_pos) {
+    return fail(MOE_ERR_NULL, "expert_out and token_topk_to_pos must not be NULL");
+  }
+  if (rows < 0) return fail(MOE_ERR_SHAPE, "rows must be >= 0");
+  if (K < 1 || K > 64) return fail(MOE_ERR_SHAPE, "K must be in [1, 64] (got %d)", K);
+  if (H <= 0 || H % 256 != 0) {
+    return fail(MOE_ERR_SHAPE, "H must be a positive multiple of 256 (got %d)", H);
+  }
+  moe::NormProblem p{expert_out, rows, token_topk_to_pos, topk_weights, K, residual, gamma_post,
+                     gate, gate_kind, alpha, gamma_pre, eps, T, H, dtype, res_dtype, residual_out,
+                     h, quant, codes, scales, false};
+  return run_norm(p, static_cast<hipStream_t>(stream), "moe_reduce_norm launch");
 }
 
 }  // extern "C"

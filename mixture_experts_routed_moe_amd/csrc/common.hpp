@@ -92,6 +92,32 @@ __device__ __forceinline__ uint32_t pk4_fp8e4m3(float a, float b, float c, float
   return u;
 }
 
+// E8M0 exponent byte of an MX block with largest magnitude amax: floor(log2 amax) -
+// emax_elem + 127 (emax_elem 8 for E4M3, 2 for E2M1), in [0, 254]; 127 for a zero block.
+__device__ __forceinline__ int mx_scale_exp(float amax, int emax_elem) {
+  if (!(amax > 0.0f)) return 127;
+  int e2;
+  frexpf(amax, &e2);                        // amax = f * 2^e2, f in [0.5, 1)
+  const int e = (e2 - 1) - emax_elem + 127;
+  return e < 0 ? 0 : (e > 254 ? 254 : e);
+}
+
+// Nearest E2M1 code (ties to the even code, saturating at 6; NaN -> 0).
+__device__ __forceinline__ uint32_t float_to_fp4e2m1(float v) {
+  const float a = fabsf(v);
+  uint32_t c;
+  if (!(a == a)) return 0u;
+  if (a <= 0.25f) c = 0u;
+  else if (a < 0.75f) c = 1u;
+  else if (a <= 1.25f) c = 2u;
+  else if (a < 1.75f) c = 3u;
+  else if (a <= 2.5f) c = 4u;
+  else if (a < 3.5f) c = 5u;
+  else if (a <= 5.0f) c = 6u;
+  else c = 7u;
+  return (v < 0.0f && c != 0u) ? (c | 8u) : c;
+}
+
 template <int DT>
 __device__ __forceinline__ float to_float(uint32_t bits16) {
   if constexpr (DT == kBF16) return bf16_to_float(bits16);

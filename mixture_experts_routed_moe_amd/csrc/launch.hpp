@@ -107,4 +107,29 @@ hipError_t launch_reduce(const void* x, int64_t rows, const int32_t* pos, const 
                          const float* x_sf, const float* sf, int T, int K, int H, int in_dtype,
                          int out_dtype, void* y, hipStream_t stream);
 
+// The norms around a block (block_norm.hip). pos != nullptr: y is expert_out
+// [rows, H] and is combined per token first.
+struct NormProblem {
+  const void* y;            // block output [T, H] of dtype, or nullptr (no block yet)
+  int64_t rows;
+  const int32_t* pos;       // token_topk_to_pos [T, K]
+  const float* w;           // topk_weights [T, K], or nullptr = ones
+  int K;
+  const void* res;          // [T, H] of res_dtype
+  const float* gamma_post;  // [H], or nullptr = no norm of y
+  const void* gate;
+  int gate_kind;
+  float alpha;
+  const float* gamma_pre;   // [H], or nullptr = no h
+  float eps;
+  int T, H, dtype, res_dtype;
+  void* res_out;
+  void* h;
+  int quant;
+  void* codes;
+  void* scales;
+  bool vec;                 // rows of 8-value vectors: H % 8 == 0, every base 16-byte aligned
+};
+hipError_t launch_block_norm(const NormProblem& p, hipStream_t stream);
+
 }  // namespace moe
