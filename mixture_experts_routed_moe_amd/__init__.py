@@ -49,11 +49,13 @@ _TABLE_FIELDS = {
 
 
 def _stream(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    """Address of the device's current stream (torch.cuda.current_stream builds
+    a Stream object for it: 2 us of a call's 20)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else None
+    return None if t is None else t.data_ptr()
 
 
 def _require(cond, status, msg):
@@ -62,6 +64,12 @@ def _require(cond, status, msg):
 
 
 def _check_tensor(t, name, dtype=None, ndim=None, device=None):
+    # Messages are only made for what fails: formatting all of them took most
+    # of a small call's time on the host.
+    if (t is not None and t.is_cuda and (device is None or t.device == device)
+            and (dtype is None or t.dtype == dtype) and (ndim is None or t.dim() == ndim)
+            and t.is_contiguous()):
+        return
     _require(t is not None, MOE_ERR_NULL, "%s must not be None" % name)
     _require(t.is_cuda, MOE_ERR_SHAPE, "%s must be a GPU tensor" % name)
     if device is not None:
@@ -948,10 +956,6 @@ def _on(device):
     return _NO_GUARD if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
-def _address(t):
-    return None if t is None else t.data_ptr()
-
-
 _GATE_NONE, _GATE_CHANNEL, _GATE_TOKEN, _GATE_FULL = 0, 1, 2, 3
 # quant= of the norm calls: MOE_QUANT_* code, dtype of the codes
 _NORM_QUANT = {"fp8": (1, torch.uint8), "int8": (2, torch.int8), "mxfp8": (3, torch.uint8),
@@ -959,7 +963,7 @@ _NORM_QUANT = {"fp8": (1, torch.uint8), "int8": (2, torch.int8), "mxfp8": (3, to
 
 
 def _norm_gate(gate, T, H, dtype, device):
-    """(MOE_GATE_* code) of a gate: float32 [H], float32 [T, 1] or dtype [T, H]."""
+    """MOE_GATE_* code of a gate: float32 [H], float32 [T, 1] or dtype [T, H]."""
     if gate is None:
         return _GATE_NONE
     _check_tensor(gate, "gate", None, None, device)
@@ -968,11 +972,21 @@ def _norm_gate(gate, T, H, dtype, device):
         return _GATE_CHANNEL
     if shape == (T, 1) and gate.dtype == torch.float32:
         return _GATE_TOKEN
-    _require(shape in ((H,), (T, 1), (T, H)), MOE_ERR_SHAPE,
-             "gate must be [%d], [%d, 1] or [%d, %d] (got %s)" % (H, T, T, H, shape))
-    _require(shape == (T, H) and gate.dtype == dtype, MOE_ERR_DTYPE,
-             "gate must be float32 [H], float32 [T, 1] or %s [T, H] (got %s)" % (dtype, gate.dtype))
+    if shape != (T, H) or gate.dtype != dtype:
+        raise MoeError(MOE_ERR_DTYPE if shape in ((H,), (T, 1), (T, H)) else MOE_ERR_SHAPE,
+                       "gate must be float32 [%d], float32 [%d, 1] or %s [%d, %d] (got %s %s)"
+                       % (H, T, dtype, T, H, gate.dtype, shape))
     return _GATE_FULL
+
+
+def _output(t, name, shape, dtype, device):
+    """An output tensor: the caller's, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _check_tensor(t, name, dtype, len(shape), device)
+    if t.shape != shape:
+        raise MoeError(MOE_ERR_SHAPE, "%s must be %s (got %s)" % (name, shape, tuple(t.shape)))
+    return t
 
 
 def _run_norm(fn, head, dtype, T, H, residual, gamma_post, gamma_pre, gate, alpha, eps, quant,
@@ -980,53 +994,43 @@ def _run_norm(fn, head, dtype, T, H, residual, gamma_post, gamma_pre, gate, alph
     """Checks and call shared by moe_block_norm and moe_reduce_norm; `head` are the
     arguments in front of `residual`."""
     dev = residual.device
-    _require(dtype in _DTYPE_CODE, MOE_ERR_DTYPE, "activations must be float16, bfloat16 or float32")
-    _require(residual.dtype in (dtype, torch.float32), MOE_ERR_DTYPE,
-             "residual must be %s or float32 (got %s)" % (dtype, residual.dtype))
+    code = _DTYPE_CODE.get(dtype)
+    if code is None:
+        raise MoeError(MOE_ERR_DTYPE, "activations must be float16, bfloat16 or float32 (got %s)" % dtype)
+    if residual.dtype != dtype and residual.dtype != torch.float32:
+        raise MoeError(MOE_ERR_DTYPE, "residual must be %s or float32 (got %s)" % (dtype, residual.dtype))
     for n, g in (("gamma_post", gamma_post), ("gamma_pre", gamma_pre)):
         if g is not None:
             _check_tensor(g, n, torch.float32, 1, dev)
-            _require(g.shape[0] == H, MOE_ERR_SHAPE, "%s must be [%d]" % (n, H))
+            if g.shape[0] != H:
+                raise MoeError(MOE_ERR_SHAPE, "%s must be [%d]" % (n, H))
     kind = _norm_gate(gate, T, H, dtype, dev)
-    _require(quant is None or quant in _NORM_QUANT, MOE_ERR_UNSUPPORTED,
-             "quant must be None or one of %s (got %r)" % (", ".join(sorted(_NORM_QUANT)), quant))
     if has_y:
-        if residual_out is None:
-            residual_out = torch.empty_like(residual)
-        _check_tensor(residual_out, "residual_out", residual.dtype, 2, dev)
-        _require(tuple(residual_out.shape) == (T, H), MOE_ERR_SHAPE, "residual_out must be [T, H]")
-    else:
-        _require(residual_out is None, MOE_ERR_NULL, "without y there is no residual_out")
-    qcode = 0
+        residual_out = _output(residual_out, "residual_out", (T, H), residual.dtype, dev)
+    elif residual_out is not None:
+        raise MoeError(MOE_ERR_NULL, "without y there is no residual_out")
     if gamma_pre is not None:
-        if h is None:
-            h = torch.empty((T, H), dtype=dtype, device=dev)
-        _check_tensor(h, "h", dtype, 2, dev)
-        _require(tuple(h.shape) == (T, H), MOE_ERR_SHAPE, "h must be [T, H]")
-    else:
-        _require(h is None and quant is None, MOE_ERR_NULL, "h and codes need gamma_pre")
+        h = _output(h, "h", (T, H), dtype, dev)
+    elif h is not None or quant is not None:
+        raise MoeError(MOE_ERR_NULL, "h and codes need gamma_pre")
+    qcode = 0
     if quant is not None:
+        if quant not in _NORM_QUANT:
+            raise MoeError(MOE_ERR_UNSUPPORTED, "quant must be None or one of %s (got %r)"
+                           % (", ".join(sorted(_NORM_QUANT)), quant))
         qcode, ctype = _NORM_QUANT[quant]
-        mx = quant.startswith("mx")
-        cshape = (T, H // 2) if quant == "mxfp4" else (T, H)
-        sshape, stype = ((T, H // 32), torch.uint8) if mx else ((T,), torch.float32)
-        if codes is None:
-            codes = torch.empty(cshape, dtype=ctype, device=dev)
-        if scales is None:
-            scales = torch.empty(sshape, dtype=stype, device=dev)
-        _check_tensor(codes, "codes", ctype, 2, dev)
-        _check_tensor(scales, "scales", stype, len(sshape), dev)
-        _require(tuple(codes.shape) == cshape and tuple(scales.shape) == sshape, MOE_ERR_SHAPE,
-                 "codes must be %s and scales %s" % (cshape, sshape))
-    else:
-        _require(codes is None and scales is None, MOE_ERR_NULL, "codes and scales need a quant")
-    if T == 0:
-        return (residual_out, h) if quant is None else (residual_out, h, codes, scales)
-    with _on(dev):
-        check(fn(*head, _address(residual), _address(gamma_post), _address(gate), kind, alpha,
-                 _address(gamma_pre), eps, T, H, _DTYPE_CODE[dtype], _DTYPE_CODE[residual.dtype],
-                 _address(residual_out), _address(h), qcode, _address(codes), _address(scales),
-                 _stream(dev)))
+        codes = _output(codes, "codes", (T, H // 2) if quant == "mxfp4" else (T, H), ctype, dev)
+        if quant.startswith("mx"):
+            scales = _output(scales, "scales", (T, H // 32), torch.uint8, dev)
+        else:
+            scales = _output(scales, "scales", (T,), torch.float32, dev)
+    elif codes is not None or scales is not None:
+        raise MoeError(MOE_ERR_NULL, "codes and scales need a quant")
+    if T:
+        with _on(dev):
+            check(fn(*head, _ptr(residual), _ptr(gamma_post), _ptr(gate), kind, alpha,
+                     _ptr(gamma_pre), eps, T, H, code, _DTYPE_CODE[residual.dtype],
+                     _ptr(residual_out), _ptr(h), qcode, _ptr(codes), _ptr(scales), _stream(dev)))
     return (residual_out, h) if quant is None else (residual_out, h, codes, scales)
 
 
@@ -1048,12 +1052,14 @@ def moe_block_norm(y, residual, gamma_post=None, gamma_pre=None, gate=None, alph
     T, H = residual.shape
     if y is not None:
         _check_tensor(y, "y", None, 2, residual.device)
-        _require(tuple(y.shape) == (T, H), MOE_ERR_SHAPE, "y must be [T, H] = %s" % ((T, H),))
-        _require(dtype is None or dtype == y.dtype, MOE_ERR_DTYPE, "dtype is y's")
+        if y.shape != residual.shape:
+            raise MoeError(MOE_ERR_SHAPE, "y must be [T, H] = %s" % ((T, H),))
+        if dtype is not None and dtype != y.dtype:
+            raise MoeError(MOE_ERR_DTYPE, "dtype is y's")
         dtype = y.dtype
     elif dtype is None:
         dtype = residual.dtype
-    return _run_norm(lib().moe_block_norm, (_address(y),), dtype, T, H, residual, gamma_post,
+    return _run_norm(lib().moe_block_norm, (_ptr(y),), dtype, T, H, residual, gamma_post,
                      gamma_pre, gate, alpha, eps, quant, residual_out, h, codes, scales, y is not None)
 
 
@@ -1069,14 +1075,15 @@ def moe_reduce_norm(expert_out, token_topk_to_pos, topk_weights, residual, gamma
     T, H = residual.shape
     dev = residual.device
     _check_tensor(expert_out, "expert_out", None, 2, dev)
-    _require(expert_out.shape[1] == H, MOE_ERR_SHAPE, "expert_out must be [rows, %d]" % H)
     _check_tensor(token_topk_to_pos, "token_topk_to_pos", torch.int32, 2, dev)
-    _require(token_topk_to_pos.shape[0] == T, MOE_ERR_SHAPE, "token_topk_to_pos must be [%d, K]" % T)
+    if expert_out.shape[1] != H or token_topk_to_pos.shape[0] != T:
+        raise MoeError(MOE_ERR_SHAPE, "expert_out must be [rows, %d] and token_topk_to_pos [%d, K]" % (H, T))
     K = token_topk_to_pos.shape[1]
     if topk_weights is not None:
         _check_tensor(topk_weights, "topk_weights", torch.float32, 2, dev)
-        _require(tuple(topk_weights.shape) == (T, K), MOE_ERR_SHAPE, "topk_weights must be [%d, %d]" % (T, K))
-    head = (_address(expert_out), expert_out.shape[0], _address(token_topk_to_pos),
-            _address(topk_weights), K)
+        if topk_weights.shape != token_topk_to_pos.shape:
+            raise MoeError(MOE_ERR_SHAPE, "topk_weights must be [%d, %d]" % (T, K))
+    head = (_ptr(expert_out), expert_out.shape[0], _ptr(token_topk_to_pos),
+            _ptr(topk_weights), K)
     return _run_norm(lib().moe_reduce_norm, head, expert_out.dtype, T, H, residual, gamma_post,
                      gamma_pre, gate, alpha, eps, quant, residual_out, h, codes, scales, True)
