@@ -560,6 +560,53 @@ moe_status moe_reduce_norm(const void* expert_out, int64_t rows,
                            int H, int dtype, int res_dtype, void* residual_out, void* h, int quant,
                            void* codes, void* scales, void* stream);
 
+/* A whole layer for a few tokens (1 <= T <= MOE_FEW_MAX_TOKENS): the router,
+ * the experts and the combine, without dispatch tables,
+ *   y[t] = R( sum over t's experts e of w(t,e) * Down_e(SiLU(g) * u) ),
+ *   g = Gate_e x[t], u = Up_e x[t], all sums and SiLU(g) * u in 32 bits, one
+ *   rounding, of y.
+ * Routing: with w_router (fp32 [E, H]; bias fp32 [E] or NULL)
+ *   logits[t, e] = R32(x[t] . w_router[e] + bias[e]), the sum in fp64,
+ *   topk_ids[t]  = the K largest, descending, ties to the lower index,
+ *   topk_weights = their softmax scores, divided by their sum if renorm,
+ * both written (int32 / fp32 [T, K]); finite inputs. With w_router NULL they
+ * are inputs: ids < 0 or >= E are masked slots (a token without slots gets
+ * zeros), an id may appear twice in a token (its weights add up),
+ * topk_weights may be NULL (ones); bias must be NULL and renorm is ignored.
+ *   x [T, H] and y [T, H] of dtype (MOE_F16 or MOE_BF16); weights as the
+ *   general calls take them: moe_layer_few 16-bit of dtype, _w8 FP8 E4M3 codes
+ *   with fp32 row scales, _mx MXFP4 codes with E8M0 scales (x and h are not
+ *   quantised: products of the weights' values with x and h).
+ *   workspace: moe_few_workspace_bytes, 256-byte aligned; it holds the logits
+ *   [T, E] at offset 0 and is written by every call (calls that overlap on
+ *   two streams need one each).
+ * Requires H % 256 == 0, D % 128 == 0 (_mx: D % 256 == 0), 1 <= E <= 1024,
+ * 1 <= K <= 64 (and K <= E with w_router); x, weights, codes and MXFP4
+ * codes on 16-byte boundaries. T == 0 returns MOE_OK and launches nothing.
+ * Two kernels (three with w_router), no atomics on memory: results do not
+ * depend on the run. Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE,
+ * MOE_ERR_UNSUPPORTED (T > MOE_FEW_MAX_TOKENS), MOE_ERR_WORKSPACE,
+ * MOE_ERR_HIP. */
+#define MOE_FEW_MAX_TOKENS 16
+size_t moe_few_workspace_bytes(int T, int K, int E, int D);
+moe_status moe_layer_few(const void* x, const float* w_router, const float* bias,
+                         const void* w_gate, const void* w_up, const void* w_down, int T, int H,
+                         int D, int E, int K, int renorm, int dtype, int32_t* topk_ids,
+                         float* topk_weights, void* workspace, size_t workspace_bytes, void* y,
+                         void* stream);
+moe_status moe_layer_few_w8(const void* x, const float* w_router, const float* bias,
+                            const uint8_t* w_gate, const uint8_t* w_up, const uint8_t* w_down,
+                            const float* s_gate, const float* s_up, const float* s_down, int T,
+                            int H, int D, int E, int K, int renorm, int dtype, int32_t* topk_ids,
+                            float* topk_weights, void* workspace, size_t workspace_bytes, void* y,
+                            void* stream);
+moe_status moe_layer_few_mx(const void* x, const float* w_router, const float* bias,
+                            const uint8_t* w_gate, const uint8_t* w_up, const uint8_t* w_down,
+                            const uint8_t* s_gate, const uint8_t* s_up, const uint8_t* s_down,
+                            int T, int H, int D, int E, int K, int renorm, int dtype,
+                            int32_t* topk_ids, float* topk_weights, void* workspace,
+                            size_t workspace_bytes, void* y, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

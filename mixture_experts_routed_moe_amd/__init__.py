@@ -30,7 +30,8 @@ __all__ = ["MoeError", "MoeTables", "FP8Weights", "default_block_m", "moe_gate",
            "moe_expert_gate_up_w4a8", "moe_expert_down_w4a8", "forward_w4a8_workspace",
            "moe_routed_forward_w4a8", "MX_FP8", "MX_FP4", "MXWeights", "quantize_mx_rows",
            "quantize_mx_weights", "moe_expert_gate_up_mx", "moe_expert_down_mx",
-           "forward_mx_workspace", "moe_routed_forward_mx", "moe_block_norm", "moe_reduce_norm"]
+           "forward_mx_workspace", "moe_routed_forward_mx", "moe_block_norm", "moe_reduce_norm",
+           "few_workspace", "moe_layer_few", "moe_layer_few_routed"]
 
 MX_FP8, MX_FP4 = 0, 4
 
@@ -1087,3 +1088,102 @@ def moe_reduce_norm(expert_out, token_topk_to_pos, topk_weights, residual, gamma
             _ptr(topk_weights), K)
     return _run_norm(lib().moe_reduce_norm, head, expert_out.dtype, T, H, residual, gamma_post,
                      gamma_pre, gate, alpha, eps, quant, residual_out, h, codes, scales, True)
+
+
+FEW_MAX_TOKENS = 16   # MOE_FEW_MAX_TOKENS of the C header
+
+
+def few_workspace(T, K, E, D, device):
+    """A workspace for moe_layer_few of T tokens with K slots each."""
+    nbytes = lib().moe_few_workspace_bytes(T, K, E, D)
+    if nbytes == 0:
+        raise MoeError(MOE_ERR_SHAPE, lib().moe_last_error().decode())
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _few(x, w_router, bias, w_gate, w_up, w_down, K, renorm, ids, weights, workspace, y):
+    """Checks and call shared by moe_layer_few and moe_layer_few_routed."""
+    _check_tensor(x, "x", None, 2)
+    dev = x.device
+    T, H = x.shape
+    if x.dtype not in (torch.float16, torch.bfloat16):
+        raise MoeError(MOE_ERR_DTYPE, "x must be float16 or bfloat16 (got %s)" % x.dtype)
+    kind = type(w_gate)
+    for n, w in (("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down)):
+        if type(w) is not kind:
+            raise MoeError(MOE_ERR_DTYPE, "the weights must be of one kind (%s is %s)" % (n, type(w).__name__))
+        if kind is FP8Weights:
+            _check_tensor(w.codes, n, torch.uint8, 3, dev)
+        elif kind is MXWeights:
+            _check_tensor(w.packed, n, torch.uint8, 3, dev)
+        else:
+            _check_tensor(w, n, x.dtype, 3, dev)
+    E, D = w_gate.shape[:2]
+    if w_gate.shape[2] != H or w_up.shape != w_gate.shape or tuple(w_down.shape) != (E, H, D):
+        raise MoeError(MOE_ERR_SHAPE, "weights must be [E, D, %d], [E, D, %d] and [E, %d, D] (got %s, %s, %s)"
+                       % (H, H, H, tuple(w_gate.shape), tuple(w_up.shape), tuple(w_down.shape)))
+    if workspace is None:
+        workspace = few_workspace(T, K, E, D, dev)
+    _check_tensor(workspace, "workspace", torch.uint8, 1, dev)
+    y = _output(y, "y", (T, H), x.dtype, dev)
+    if T:
+        if kind is FP8Weights:
+            fn = lib().moe_layer_few_w8
+            w = (_ptr(w_gate.codes), _ptr(w_up.codes), _ptr(w_down.codes), _ptr(w_gate.scales),
+                 _ptr(w_up.scales), _ptr(w_down.scales))
+        elif kind is MXWeights:
+            fn = lib().moe_layer_few_mx
+            w = (_ptr(w_gate.packed), _ptr(w_up.packed), _ptr(w_down.packed), _ptr(w_gate.scales),
+                 _ptr(w_up.scales), _ptr(w_down.scales))
+        else:
+            fn = lib().moe_layer_few
+            w = (_ptr(w_gate), _ptr(w_up), _ptr(w_down))
+        with _on(dev):
+            check(fn(_ptr(x), _ptr(w_router), _ptr(bias), *w, T, H, D, E, K, int(bool(renorm)),
+                     _DTYPE_CODE[x.dtype], _ptr(ids), _ptr(weights), _ptr(workspace),
+                     workspace.numel(), _ptr(y), _stream(dev)))
+    return y
+
+
+def moe_layer_few(x, w_router, w_gate, w_up, w_down, top_k, renorm=True, bias=None, y=None,
+                  topk_ids=None, topk_weights=None, workspace=None):
+    """A whole layer (router, experts, combine) for at most FEW_MAX_TOKENS
+    tokens: x [T, H] float16 / bfloat16, w_router float32 [E, H], bias float32
+    [E] or None, expert weights as tensors of x's dtype, FP8Weights or MXWeights.
+    Logits are fp64 sums rounded to fp32, ties go to the lower expert; the
+    experts' hidden values stay in 32 bits and y is rounded once.
+    Returns (y [T, H], topk_ids int32 [T, K], topk_weights float32 [T, K])."""
+    _check_tensor(x, "x", None, 2)
+    dev = x.device
+    K = int(top_k)
+    _check_tensor(w_router, "w_router", torch.float32, 2, dev)
+    if tuple(w_router.shape) != (w_gate.shape[0], x.shape[1]):
+        raise MoeError(MOE_ERR_SHAPE, "w_router must be [%d, %d] (got %s)"
+                       % (w_gate.shape[0], x.shape[1], tuple(w_router.shape)))
+    if bias is not None:
+        _check_tensor(bias, "bias", torch.float32, 1, dev)
+        if bias.shape[0] != w_router.shape[0]:
+            raise MoeError(MOE_ERR_SHAPE, "bias must be [%d]" % w_router.shape[0])
+    if K < 1 or K > min(64, w_router.shape[0]):
+        raise MoeError(MOE_ERR_SHAPE, "top_k must be in [1, min(E, 64)] (got %d)" % K)
+    shape = (x.shape[0], K)
+    topk_ids = _output(topk_ids, "topk_ids", shape, torch.int32, dev)
+    topk_weights = _output(topk_weights, "topk_weights", shape, torch.float32, dev)
+    y = _few(x, w_router, bias, w_gate, w_up, w_down, K, renorm, topk_ids, topk_weights, workspace, y)
+    return y, topk_ids, topk_weights
+
+
+def moe_layer_few_routed(x, topk_ids, topk_weights, w_gate, w_up, w_down, y=None, workspace=None):
+    """moe_layer_few with the routing given: topk_ids int32 [T, K] (negative or
+    >= E = masked slot; an id twice in a token: its weights add up),
+    topk_weights float32 [T, K] or None (ones). Returns y [T, H]."""
+    _check_tensor(x, "x", None, 2)
+    _check_tensor(topk_ids, "topk_ids", torch.int32, 2, x.device)
+    if topk_ids.shape[0] != x.shape[0]:
+        raise MoeError(MOE_ERR_SHAPE, "topk_ids must be [%d, K]" % x.shape[0])
+    if topk_weights is not None:
+        _check_tensor(topk_weights, "topk_weights", torch.float32, 2, x.device)
+        if topk_weights.shape != topk_ids.shape:
+            raise MoeError(MOE_ERR_SHAPE, "topk_weights must be %s" % (tuple(topk_ids.shape),))
+    return _few(x, None, None, w_gate, w_up, w_down, topk_ids.shape[1], False, topk_ids,
+                topk_weights, workspace, y)

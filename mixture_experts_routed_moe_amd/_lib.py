@@ -141,6 +141,15 @@ def lib():
         L.moe_block_norm.restype = i32
         L.moe_reduce_norm.argtypes = [vp, i64, vp, vp, i32] + norm
         L.moe_reduce_norm.restype = i32
+        L.moe_few_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        L.moe_few_workspace_bytes.restype = sz
+        few = [i32] * 7 + [vp, vp, vp, sz, vp, vp]
+        L.moe_layer_few.argtypes = [vp] * 6 + few
+        L.moe_layer_few.restype = i32
+        L.moe_layer_few_w8.argtypes = [vp] * 9 + few
+        L.moe_layer_few_w8.restype = i32
+        L.moe_layer_few_mx.argtypes = [vp] * 9 + few
+        L.moe_layer_few_mx.restype = i32
         _lib = L
     return _lib
 

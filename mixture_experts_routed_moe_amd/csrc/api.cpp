@@ -940,4 +940,98 @@ moe_status moe_reduce_norm(const void* expert_out, int64_t rows,
   return run_norm(p, static_cast<hipStream_t>(stream), "moe_reduce_norm launch");
 }
 
+static moe_status few_sizes(int T, int K, int E, int D) {
+  if (T < 0) return fail(MOE_ERR_SHAPE, "T must be >= 0 (got %d)", T);
+  if (T > MOE_FEW_MAX_TOKENS) {
+    return fail(MOE_ERR_UNSUPPORTED, "the layer for few tokens takes at most %d (got %d)",
+                MOE_FEW_MAX_TOKENS, T);
+  }
+  if (K < 1 || K > 64) return fail(MOE_ERR_SHAPE, "K must be in [1, 64] (got %d)", K);
+  if (E < 1 || E > 1024) return fail(MOE_ERR_SHAPE, "E must be in [1, 1024] (got %d)", E);
+  if (D <= 0 || D % 128 != 0) return fail(MOE_ERR_SHAPE, "D must be a positive multiple of 128 (got %d)", D);
+  return MOE_OK;
+}
+
+static size_t few_logits_bytes(int T, int E) { return align_up(4 * static_cast<size_t>(T) * E); }
+
+size_t moe_few_workspace_bytes(int T, int K, int E, int D) {
+  if (few_sizes(T, K, E, D) != MOE_OK) return 0;
+  const int rows = T > 0 ? T : 1;
+  return few_logits_bytes(rows, E) + align_up(4 * static_cast<size_t>(rows) * K * D);
+}
+
+static moe_status run_few(moe::FewProblem& p, void* workspace, size_t workspace_bytes,
+                          hipStream_t stream, const char* what) {
+  moe_status s = few_sizes(p.T, p.K, p.E, p.D);
+  if (s != MOE_OK) return s;
+  if (!p.x || !p.wg || !p.wu || !p.wd || !p.ids || !workspace || !p.y) {
+    return fail(MOE_ERR_NULL, "x, the weights, topk_ids, workspace and y must not be NULL");
+  }
+  if (p.fmt != moe::kFewW16 && (!p.sg || !p.su || !p.sd)) {
+    return fail(MOE_ERR_NULL, "the weights' scales must not be NULL");
+  }
+  if (p.w_router && !p.weights) return fail(MOE_ERR_NULL, "topk_weights must not be NULL with w_router");
+  if (!p.w_router && p.bias) return fail(MOE_ERR_NULL, "bias needs w_router");
+  if (p.w_router && p.K > p.E) {
+    return fail(MOE_ERR_SHAPE, "K must be in [1, min(E, 64)] (got K=%d, E=%d)", p.K, p.E);
+  }
+  if (p.H <= 0 || p.H % 256 != 0) return fail(MOE_ERR_SHAPE, "H must be a positive multiple of 256 (got %d)", p.H);
+  if (p.fmt == moe::kFewMx && p.D % 256 != 0) {
+    return fail(MOE_ERR_SHAPE, "MXFP4 weights need D a multiple of 256 (got %d)", p.D);
+  }
+  // lane offsets are 32 bits: 16 rows of x or of a weight, the hidden rows
+  if (p.H > (1 << 24) || static_cast<int64_t>(p.T) * p.K * p.D > (int64_t{1} << 28)) {
+    return fail(MOE_ERR_SHAPE, "H or T * K * D too large");
+  }
+  if (!is_16bit(p.dtype)) return fail(MOE_ERR_DTYPE, "dtype must be MOE_F16 or MOE_BF16");
+  uintptr_t bits = 0;
+  for (const void* q : {p.x, p.wg, p.wu, p.wd, static_cast<const void*>(p.w_router)}) {
+    bits |= reinterpret_cast<uintptr_t>(q);
+  }
+  if (bits % 16 != 0) return fail(MOE_ERR_SHAPE, "x, w_router and the weights must be 16-byte aligned");
+  const size_t need = moe_few_workspace_bytes(p.T, p.K, p.E, p.D);
+  if (workspace_bytes < need) {
+    return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+  }
+  if (reinterpret_cast<uintptr_t>(workspace) % kAlign != 0) {
+    return fail(MOE_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  }
+  if (p.T == 0) return ok();
+  p.logits = static_cast<float*>(workspace);
+  p.hw = static_cast<char*>(workspace) + few_logits_bytes(p.T, p.E);
+  return hip_status(moe::launch_few(p, stream), what);
+}
+
+moe_status moe_layer_few(const void* x, const float* w_router, const float* bias,
+                         const void* w_gate, const void* w_up, const void* w_down, int T, int H,
+                         int D, int E, int K, int renorm, int dtype, int32_t* topk_ids,
+                         float* topk_weights, void* workspace, size_t workspace_bytes, void* y,
+                         void* stream) {
+  moe::FewProblem p{x, w_router, bias, w_gate, w_up, w_down, nullptr, nullptr, nullptr, T, H, D, E,
+                    K, renorm, dtype, moe::kFewW16, topk_ids, topk_weights, nullptr, nullptr, y};
+  return run_few(p, workspace, workspace_bytes, static_cast<hipStream_t>(stream), "moe_layer_few launch");
+}
+
+moe_status moe_layer_few_w8(const void* x, const float* w_router, const float* bias,
+                            const uint8_t* w_gate, const uint8_t* w_up, const uint8_t* w_down,
+                            const float* s_gate, const float* s_up, const float* s_down, int T,
+                            int H, int D, int E, int K, int renorm, int dtype, int32_t* topk_ids,
+                            float* topk_weights, void* workspace, size_t workspace_bytes, void* y,
+                            void* stream) {
+  moe::FewProblem p{x, w_router, bias, w_gate, w_up, w_down, s_gate, s_up, s_down, T, H, D, E, K,
+                    renorm, dtype, moe::kFewFp8, topk_ids, topk_weights, nullptr, nullptr, y};
+  return run_few(p, workspace, workspace_bytes, static_cast<hipStream_t>(stream), "moe_layer_few_w8 launch");
+}
+
+moe_status moe_layer_few_mx(const void* x, const float* w_router, const float* bias,
+                            const uint8_t* w_gate, const uint8_t* w_up, const uint8_t* w_down,
+                            const uint8_t* s_gate, const uint8_t* s_up, const uint8_t* s_down,
+                            int T, int H, int D, int E, int K, int renorm, int dtype,
+                            int32_t* topk_ids, float* topk_weights, void* workspace,
+                            size_t workspace_bytes, void* y, void* stream) {
+  moe::FewProblem p{x, w_router, bias, w_gate, w_up, w_down, s_gate, s_up, s_down, T, H, D, E, K,
+                    renorm, dtype, moe::kFewMx, topk_ids, topk_weights, nullptr, nullptr, y};
+  return run_few(p, workspace, workspace_bytes, static_cast<hipStream_t>(stream), "moe_layer_few_mx launch");
+}
+
 }  // extern "C"

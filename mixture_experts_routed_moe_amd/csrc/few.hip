@@ -1,0 +1,702 @@
+// A whole mixture-of-experts layer for a few tokens (T <= 16) on gfx950.
+//
+//   logits[t, e] = x[t] . Wr[e] + bias[e]          ids, w = top-k softmax of them
+//   g = x[t] . W_gate[e, d],  u = x[t] . W_up[e, d]
+//   hw[t, e, d] = (sum of w over t's slots that name e) * SiLU(g) * u
+//   y[t, c] = R( sum over t's experts e ascending of hw[t, e] . W_down[e, c] )
+//
+// Bound: the weights of the distinct experts, read once. With so few tokens
+// every matrix product is a stream of weight rows against at most 16 rows of
+// activations, one v_mfma 16x16x32 tile high, so the kernels are built around
+// the stream and the dispatch tables, the sorted rows, expert_out and the
+// separate reduce of the general path all go away:
+//
+//   few_logits_kernel   one workgroup an expert, all tokens: sums in fp64 (the
+//                       products of 16-bit and fp32 values are exact there), so
+//                       ids do not hang on a summation order; fp64 vector FMAs
+//                       run at the fp32 rate and the kernel waits for memory.
+//   few_gate_up_kernel  every workgroup repeats the top-k selection in its
+//                       prologue (a few LDS-sized arrays; cheaper than a launch
+//                       and a pass through memory), finds the distinct experts
+//                       and takes (expert, 16 columns) items in turn. Its 4
+//                       waves split the reduction; partial sums meet in LDS.
+//   few_down_kernel     one workgroup per 16 columns of y walks ALL distinct
+//                       experts: row t of the MFMA tile is token t, so one
+//                       accumulator holds y itself and no pass combines expert
+//                       rows. Its waves split the (expert, reduction) stream.
+//
+// Both GEMM kernels run one uninterrupted stream of chunks (64 bytes of each
+// of 16 weight rows = 1 KB a load) through a register ring that crosses item
+// and expert borders. MFMA rows of tokens that an expert does not serve read
+// a served token's row and are left out where sums are added up (a select:
+// nothing of an expert, not even a NaN, reaches a token that it does not
+// serve).
+//
+// Precision: hw stays in 32 bits between the kernels. bf16, FP8 and MXFP4
+// weights meet it as a pair of bf16 (16 significant bits; a single bf16 would
+// double the error variance of a bf16 y), fp16 weights meet it in fp32 on
+// v_mfma_f32_16x16x4 (fp16 pairs would overflow past 65504; at 16 rows the
+// fp32 instruction still outruns the weight stream: 8 x 32 cycles per 1 KB a
+// wave, 16 B/clk/CU against the 10 that HBM delivers). FP8 codes are exact in
+// 16 bits; MXFP4 codes times their E8M0 scale are exact in bf16, so fp16
+// activations against MXFP4 weights are split into two bf16 (exact).
+
+#include "common.hpp"
+#include "launch.hpp"
+
+namespace moe {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kRows = 16;                        // tokens of one call at most
+constexpr int kMaxE = 1024;
+constexpr int kMaxP = kRows * 64;                // routed pairs at most
+constexpr int kGateUpThreads = 256;
+constexpr int kW16 = 0, kWFp8 = 1, kWMx = 2;     // weight formats
+
+// Reduction elements in 16 bytes of one weight row.
+template <int F>
+constexpr int lane_elems() {
+  return F == kW16 ? 8 : (F == kWFp8 ? 16 : 32);
+}
+
+struct FewArgs {
+  const void* x;
+  const uint8_t *wg, *wu, *wd;
+  const void *sg, *su, *sd;       // FP8: fp32 per row; MXFP4: E8M0 per 32 elements
+  const float* logits;            // nullptr: ids and weights are given
+  int32_t* ids;
+  float* weights;
+  uint8_t* hw;                    // [P, D] fp32, or two [P, D] bf16 (high, low parts)
+  void* y;
+  int T, H, D, E, K, renorm;
+};
+
+// ---------------------------------------------------------------- router --
+
+// Logits of expert blockIdx.x for TT >= T tokens: every thread strides over
+// the row four elements at a time, fp64 sums go lane -> wave -> workgroup.
+template <int DT, int TT>
+__global__ __launch_bounds__(256) void few_logits_kernel(const uint16_t* __restrict__ x,
+                                                         const float* __restrict__ wr,
+                                                         const float* __restrict__ bias, int T,
+                                                         int H, int E, float* __restrict__ logits) {
+  __shared__ double part[4][TT];
+  const int e = blockIdx.x, tid = threadIdx.x;
+  double acc[TT];
+#pragma unroll
+  for (int t = 0; t < TT; ++t) acc[t] = 0.0;
+  const float* row = wr + static_cast<int64_t>(e) * H;
+#pragma unroll 2
+  for (int c = tid * 4; c < H; c += 1024) {
+    const float4 w = *reinterpret_cast<const float4*>(row + c);
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      const int tt = t < T ? t : 0;
+      const u32x2 v = *reinterpret_cast<const u32x2*>(x + static_cast<int64_t>(tt) * H + c);
+      acc[t] = fma(static_cast<double>(to_float<DT>(v.x & 0xffffu)), static_cast<double>(w.x), acc[t]);
+      acc[t] = fma(static_cast<double>(to_float<DT>(v.x >> 16)), static_cast<double>(w.y), acc[t]);
+      acc[t] = fma(static_cast<double>(to_float<DT>(v.y & 0xffffu)), static_cast<double>(w.z), acc[t]);
+      acc[t] = fma(static_cast<double>(to_float<DT>(v.y >> 16)), static_cast<double>(w.w), acc[t]);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < TT; ++t) {
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) acc[t] += __shfl_xor(acc[t], off);
+    if ((tid & 63) == 0) part[tid >> 6][t] = acc[t];
+  }
+  __syncthreads();
+  if (tid < T) {
+    double s = part[0][tid] + part[1][tid] + part[2][tid] + part[3][tid];
+    if (bias) s += static_cast<double>(bias[e]);
+    logits[static_cast<int64_t>(tid) * E + e] = static_cast<float>(s);
+  }
+}
+
+// ------------------------------------------------------------- selection --
+
+// Unsigned keys in the order of the floats (-0 as +0); 0 means "none".
+__device__ __forceinline__ uint32_t order_key(float f) {
+  const uint32_t u = __float_as_uint(f + 0.0f);
+  const uint32_t k = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  return k ? k : 1u;
+}
+
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+
+// The wave's largest value, in every lane: rows of 16 by DPP shifts, then
+// across the rows (lanes without a source read 0).
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#define MOE_DPP_MAX(ctrl, rows)                                                                   \
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), ctrl, rows, \
+                                                               0xf, false)))
+  MOE_DPP_MAX(0x111, 0xf);   // row_shr:1
+  MOE_DPP_MAX(0x112, 0xf);
+  MOE_DPP_MAX(0x114, 0xf);
+  MOE_DPP_MAX(0x118, 0xf);
+  MOE_DPP_MAX(0x142, 0xa);   // row_bcast:15 into rows 1 and 3
+  MOE_DPP_MAX(0x143, 0xc);   // row_bcast:31 into rows 2 and 3
+#undef MOE_DPP_MAX
+  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
+}
+
+// Top-k of one token by one wave: lane L holds experts L * NPL .. + NPL - 1,
+// so the lowest lane with the maximum holds the lowest expert index.
+template <int NPL>
+__device__ void select_topk(const float* logits, int E, int K, int renorm, int lane, int* sid,
+                            float* sw) {
+  uint32_t key[NPL];
+  uint32_t best = 0u;
+  int best_j = 0;
+#pragma unroll
+  for (int j = 0; j < NPL; ++j) {
+    const int e = lane * NPL + j;
+    key[j] = e < E ? order_key(logits[e]) : 0u;
+  }
+  auto rescan = [&]() __attribute__((always_inline)) {
+    best = key[0];
+    best_j = 0;
+#pragma unroll
+    for (int j = 1; j < NPL; ++j) {
+      if (key[j] > best) {
+        best = key[j];
+        best_j = j;
+      }
+    }
+  };
+  rescan();
+  const float top = key_value(wave_max(best));
+  float z = 0.0f;
+#pragma unroll
+  for (int j = 0; j < NPL; ++j) {
+    if (key[j]) z += expf(key_value(key[j]) - top);
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) z += __shfl_xor(z, off);
+  float mine = 0.0f;            // lane k keeps the k-th selection (K <= 64)
+  int mine_id = 0;
+  for (int k = 0; k < K; ++k) {
+    const uint32_t m = wave_max(best);
+    const int src = __builtin_ctzll(__ballot(best == m));
+    const int id = __builtin_amdgcn_readlane(lane * NPL + best_j, src);
+    if (lane == k) {
+      mine = key_value(m);
+      mine_id = id;
+    }
+    if (lane == src) {
+#pragma unroll
+      for (int j = 0; j < NPL; ++j) {
+        if (j == best_j) key[j] = 0u;
+      }
+      rescan();
+    }
+  }
+  float p = lane < K ? expf(mine - top) / z : 0.0f;
+  if (renorm) {
+    float s = p;
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off);
+    p = p / s;
+  }
+  if (lane < K) {
+    sid[lane] = mine_id;
+    sw[lane] = p;
+  }
+}
+
+// What the workgroups of both GEMM kernels know of the routing.
+struct Plan {
+  int sid[kMaxP];              // expert of each slot, -1 = masked
+  uint32_t mask[kMaxE];        // tokens of each expert
+  uint16_t list[kMaxE];        // the distinct experts, ascending
+  int count;
+};
+
+// mask, list and count from sid (written before, by any thread).
+__device__ __forceinline__ void build_plan(Plan& s, int P, int K, int E, int tid, int threads) {
+  for (int e = tid; e < E; e += threads) s.mask[e] = 0u;
+  __syncthreads();
+  for (int p = tid; p < P; p += threads) {
+    if (s.sid[p] >= 0) atomicOr(&s.mask[s.sid[p]], 1u << (p / K));
+  }
+  __syncthreads();
+  if (tid < 64) {
+    int n = 0;
+    for (int e0 = 0; e0 < E; e0 += 64) {
+      const bool used = e0 + tid < E && s.mask[e0 + tid] != 0u;
+      const uint64_t b = __ballot(used);
+      if (used) s.list[n + __popcll(b & ((1ull << tid) - 1))] = static_cast<uint16_t>(e0 + tid);
+      n += __popcll(b);
+    }
+    if (tid == 0) s.count = n;
+  }
+  __syncthreads();
+}
+
+// --------------------------------------------------------------- operands --
+
+// A value that is the same in all lanes, in a scalar register.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+template <int DT>
+__device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
+  if constexpr (DT == kBF16) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  } else {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  }
+}
+
+// 16 bytes of a weight row -> its 16-bit MFMA operands of 8 elements each
+// (dtype DT; MXFP4 always bf16, scaled by 2^(sc - 127)).
+template <int DT, int F>
+__device__ __forceinline__ void decode(u32x4 w, uint32_t sc, u32x4* out) {
+  if constexpr (F == kW16) {
+    out[0] = w;
+  } else if constexpr (F == kWFp8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t v;
+      if constexpr (DT == kBF16) {
+        v = (i & 1) ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i >> 1], 1.0f, true))
+                    : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i >> 1], 1.0f, false));
+      } else {
+        v = (i & 1) ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[i >> 1], 1.0f, true))
+                    : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[i >> 1], 1.0f, false));
+      }
+      out[i >> 2][i & 3] = v;
+    }
+  } else {
+    const float s = __uint_as_float(sc << 23);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      out[i][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i], s, 0));
+      out[i][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i], s, 1));
+      out[i][2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i], s, 2));
+      out[i][3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i], s, 3));
+    }
+  }
+}
+
+// v = high + low in bf16, |v - high - low| <= 2^-17 |v|.
+__device__ __forceinline__ void split_bf16(float v, uint32_t& hi, uint32_t& lo) {
+  hi = float_to_bf16(v);
+  // a value that rounds to infinity (or is not finite) has no remainder
+  const float r = v - bf16_to_float(hi);
+  lo = fabsf(r) <= 3.0e38f ? float_to_bf16(r) : 0u;
+}
+
+// Eight fp16 values as two bf16 operands (exact: 11 significant bits).
+__device__ __forceinline__ void split_f16x8(u32x4 x, u32x4& hi, u32x4& lo) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t h0, l0, h1, l1;
+    split_bf16(f16_to_float(x[i] & 0xffffu), h0, l0);
+    split_bf16(f16_to_float(x[i] >> 16), h1, l1);
+    hi[i] = h0 | (h1 << 16);
+    lo[i] = l0 | (l1 << 16);
+  }
+}
+
+// ---------------------------------------------------------------- gate/up --
+
+// hw in fp32 (fp16 weights) or as bf16 parts.
+template <int DT, int F>
+constexpr bool hw_fp32() {
+  return DT == kF16 && F == kW16;
+}
+
+// One chunk of a wave: 64 bytes of 16 gate and 16 up rows, the tokens' x.
+template <int F>
+struct GateUpSlot {
+  u32x4 g, u;
+  u32x4 x[lane_elems<F>() / 8];
+  uint32_t sg, su;              // FP8: the rows' fp32 scales; MXFP4: E8M0 bytes
+};
+
+template <int DT, int F>
+__global__ __launch_bounds__(kGateUpThreads, 4) void few_gate_up_kernel(FewArgs a) {
+  constexpr int EL = lane_elems<F>(), NX = EL / 8, S = F == kW16 ? 8 : (F == kWFp8 ? 5 : 3);
+  __shared__ Plan plan;
+  __shared__ float sw[kMaxP];
+  __shared__ f32x4 red[2][4][2][64];
+  const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63, lr = lane & 15, lg = lane >> 4;
+  const int P = a.T * a.K;
+
+  if (a.logits) {
+    for (int t = wave; t < a.T; t += 4) {
+      const float* l = a.logits + static_cast<int64_t>(t) * a.E;
+      int* sid = plan.sid + t * a.K;
+      float* w = sw + t * a.K;
+      if (a.E <= 64) select_topk<1>(l, a.E, a.K, a.renorm, lane, sid, w);
+      else if (a.E <= 256) select_topk<4>(l, a.E, a.K, a.renorm, lane, sid, w);
+      else select_topk<16>(l, a.E, a.K, a.renorm, lane, sid, w);
+    }
+  } else {
+    for (int p = tid; p < P; p += kGateUpThreads) {
+      const int id = a.ids[p];
+      plan.sid[p] = id >= 0 && id < a.E ? id : -1;
+      sw[p] = a.weights ? a.weights[p] : 1.0f;
+    }
+  }
+  build_plan(plan, P, a.K, a.E, tid, kGateUpThreads);
+  if (a.logits && blockIdx.x == 0) {
+    for (int p = tid; p < P; p += kGateUpThreads) {
+      a.ids[p] = plan.sid[p];
+      a.weights[p] = sw[p];
+    }
+  }
+
+  const int tiles = a.D / 16;
+  const int items = plan.count * tiles;
+  if (static_cast<int>(blockIdx.x) >= items) return;
+  // This wave's chunks of every item: pairs (128 bytes a row) wave, wave + 4, ...
+  const int pairs = a.H / (8 * EL);
+  const int n = 2 * ((pairs - wave + 3) / 4);
+  const int64_t row_bytes = static_cast<int64_t>(a.H / EL) * 16;
+  const int64_t blocks = a.H / 32;
+
+  // Where the next chunk to load lies: wave-uniform bases (scalar registers)
+  // and fixed 32-bit lane offsets.
+  int l_item = blockIdx.x, l_c = 0;
+  const uint8_t *pg = nullptr, *pu = nullptr, *qg = nullptr, *qu = nullptr;
+  const uint32_t w_off = static_cast<uint32_t>(lr * row_bytes) + lg * 16;
+  const uint32_t s_off = F == kWFp8 ? lr * 4 : static_cast<uint32_t>(lr * blocks) + lg;
+  uint32_t x_off = 0;
+  auto aim = [&]() __attribute__((always_inline)) {
+    const int e = uniform(plan.list[l_item / tiles]);
+    const int64_t row = static_cast<int64_t>(e) * a.D + (l_item % tiles) * 16;
+    pg = a.wg + row * row_bytes;
+    pu = a.wu + row * row_bytes;
+    if constexpr (F != kW16) {
+      qg = static_cast<const uint8_t*>(a.sg) + row * (F == kWFp8 ? 4 : blocks);
+      qu = static_cast<const uint8_t*>(a.su) + row * (F == kWFp8 ? 4 : blocks);
+    }
+    const uint32_t m = static_cast<uint32_t>(uniform(static_cast<int>(plan.mask[e])));
+    const int t = (m >> lr) & 1 ? lr : __builtin_ctz(m);
+    x_off = static_cast<uint32_t>(t * a.H + lg * EL) * 2;
+  };
+  GateUpSlot<F> ring[S];
+  auto load = [&](GateUpSlot<F>& s) __attribute__((always_inline)) {
+    const int64_t c = 8 * (l_c >> 1) + 2 * wave + (l_c & 1);
+    s.g = *reinterpret_cast<const u32x4*>(pg + c * 64 + w_off);
+    s.u = *reinterpret_cast<const u32x4*>(pu + c * 64 + w_off);
+    const uint8_t* px = static_cast<const uint8_t*>(a.x) + c * (8 * EL);
+#pragma unroll
+    for (int i = 0; i < NX; ++i) s.x[i] = *reinterpret_cast<const u32x4*>(px + x_off + 16 * i);
+    if constexpr (F == kWFp8) {
+      s.sg = *reinterpret_cast<const uint32_t*>(qg + s_off);
+      s.su = *reinterpret_cast<const uint32_t*>(qu + s_off);
+    } else if constexpr (F == kWMx) {
+      s.sg = (qg + c * 4)[s_off];
+      s.su = (qu + c * 4)[s_off];
+    }
+    if (++l_c == n) {
+      // past the last item the last chunk is read again (in bounds, never used)
+      if (l_item + static_cast<int>(gridDim.x) < items) {
+        l_item += gridDim.x;
+        l_c = 0;
+        aim();
+      } else {
+        l_c = n - 1;
+      }
+    }
+  };
+
+  int item = blockIdx.x, buf = 0;
+  f32x4 accg = {}, accu = {};
+  float scale_g = 1.0f, scale_u = 1.0f;
+  // The item's sums are complete: add up the waves' parts and store hw.
+  auto finish = [&]() __attribute__((always_inline)) {
+    red[buf][wave][0][lane] = accg;
+    red[buf][wave][1][lane] = accu;
+    accg = accu = f32x4{};
+    wait_lds();
+    barrier_no_wait();
+    // thread (wave i, lane l): register i of lane l, row 4 (l / 16) + i
+    float g = 0.0f, u = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      g += reinterpret_cast<const float*>(&red[buf][w][0][lane])[wave];
+      u += reinterpret_cast<const float*>(&red[buf][w][1][lane])[wave];
+    }
+    const int e = uniform(plan.list[item / tiles]);
+    const int t = lg * 4 + wave;
+    if ((plan.mask[e] >> t) & 1) {
+      int p = -1;
+      float w = 0.0f;
+      for (int k = a.K - 1; k >= 0; --k) {
+        if (plan.sid[t * a.K + k] == e) {
+          p = t * a.K + k;
+          w += sw[p];
+        }
+      }
+      if constexpr (F == kWFp8) {
+        g *= scale_g;
+        u *= scale_u;
+      }
+      const float v = w * (silu(g) * u);
+      const int64_t at = static_cast<int64_t>(p) * a.D + (item % tiles) * 16 + lr;
+      if constexpr (hw_fp32<DT, F>()) {
+        reinterpret_cast<float*>(a.hw)[at] = v;
+      } else {
+        uint32_t hi, lo;
+        split_bf16(v, hi, lo);
+        uint16_t* h = reinterpret_cast<uint16_t*>(a.hw);
+        h[at] = static_cast<uint16_t>(hi);
+        h[static_cast<int64_t>(P) * a.D + at] = static_cast<uint16_t>(lo);
+      }
+    }
+    buf ^= 1;   // the other buffer: a wave still reading this one has not passed the next barrier
+    item += gridDim.x;
+  };
+
+  if (n == 0) {                      // fewer pairs than waves: this one only adds zeros
+    if constexpr (F == kWFp8) {
+      while (item < items) {
+        const int64_t row = static_cast<int64_t>(plan.list[item / tiles]) * a.D + (item % tiles) * 16 + lr;
+        scale_g = static_cast<const float*>(a.sg)[row];
+        scale_u = static_cast<const float*>(a.su)[row];
+        finish();
+      }
+    } else {
+      while (item < items) finish();
+    }
+    return;
+  }
+  aim();
+#pragma unroll
+  for (int s = 0; s < S; ++s) load(ring[s]);
+  int c = 0;
+  auto step = [&](auto U) __attribute__((always_inline)) {
+    constexpr int s = decltype(U)::value;
+    u32x4 wg[NX], wu[NX];
+    decode<DT, F>(ring[s].g, ring[s].sg, wg);
+    decode<DT, F>(ring[s].u, ring[s].su, wu);
+#pragma unroll
+    for (int i = 0; i < NX; ++i) {
+      if constexpr (F == kWMx && DT == kF16) {
+        u32x4 hi, lo;
+        split_f16x8(ring[s].x[i], hi, lo);
+        accg = mfma16<kBF16>(hi, wg[i], accg);
+        accu = mfma16<kBF16>(hi, wu[i], accu);
+        accg = mfma16<kBF16>(lo, wg[i], accg);
+        accu = mfma16<kBF16>(lo, wu[i], accu);
+      } else {
+        accg = mfma16<DT>(ring[s].x[i], wg[i], accg);
+        accu = mfma16<DT>(ring[s].x[i], wu[i], accu);
+      }
+    }
+    if constexpr (F == kWFp8) {
+      scale_g = __uint_as_float(ring[s].sg);
+      scale_u = __uint_as_float(ring[s].su);
+    }
+    load(ring[s]);
+    if (++c == n) {
+      c = 0;
+      finish();
+    }
+  };
+  // Whole turns of the ring without a condition around a load (one would make
+  // the compiler wait for more loads than it has to), then the rest.
+  const int mine = (items - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+  const int chunks = mine * n;
+  for (int i = 0; i < chunks / S; ++i) static_for<S>(step);
+  static_for<S>([&](auto U) __attribute__((always_inline)) {
+    if (decltype(U)::value < chunks % S) step(U);
+  });
+}
+
+// ------------------------------------------------------------------- down --
+
+template <int DT, int F>
+struct DownSlot {
+  u32x4 w;
+  u32x4 h[lane_elems<F>() / 4];   // hw: fp32 (8 elements in 2), or the high parts, then the low parts
+  uint32_t s;
+};
+
+template <int DT, int F, int NW>
+__global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs a) {
+  constexpr int EL = lane_elems<F>(), NX = EL / 8, S = F == kW16 ? 8 : (F == kWFp8 ? 4 : 2);
+  __shared__ Plan plan;
+  __shared__ uint16_t pair[kMaxE * kRows];   // hw row of (distinct expert, token)
+  __shared__ f32x4 red[NW][64];
+  const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63, lr = lane & 15, lg = lane >> 4;
+  const int P = a.T * a.K;
+  for (int p = tid; p < P; p += 64 * NW) {
+    const int id = a.ids[p];
+    plan.sid[p] = id >= 0 && id < a.E ? id : -1;
+  }
+  build_plan(plan, P, a.K, a.E, tid, 64 * NW);
+  for (int i = tid; i < plan.count * kRows; i += 64 * NW) {
+    const int e = plan.list[i / kRows];
+    const uint32_t m = plan.mask[e];
+    const int t = (m >> (i % kRows)) & 1 ? i % kRows : __builtin_ctz(m);
+    int p = 0;
+    for (int k = a.K - 1; k >= 0; --k) {
+      if (plan.sid[t * a.K + k] == e) p = t * a.K + k;
+    }
+    pair[i] = static_cast<uint16_t>(p);
+  }
+  __syncthreads();
+
+  const int col = blockIdx.x * 16 + lr;
+  const int pairs = a.D / (8 * EL);                 // 128-byte pieces of a weight row
+  const int64_t row_bytes = static_cast<int64_t>(a.D / EL) * 16;
+  const int total = plan.count * pairs;
+  const int u0 = static_cast<int>(static_cast<int64_t>(total) * wave / NW);
+  const int u1 = static_cast<int>(static_cast<int64_t>(total) * (wave + 1) / NW);
+  const int chunks = 2 * pairs;                     // of one expert
+
+  f32x4 sum = {}, acc = {};
+  if (u0 < u1) {
+    int l_j = u0 / pairs, l_c = 2 * (u0 % pairs), l_left = 2 * (u1 - u0);
+    const uint8_t *pw = nullptr, *q = nullptr;
+    const uint32_t w_off = static_cast<uint32_t>(lr * row_bytes) + lg * 16;
+    const uint32_t s_off = F == kWFp8 ? lr * 4 : static_cast<uint32_t>(lr * (a.D / 32)) + lg;
+    const uint8_t* low = a.hw + static_cast<int64_t>(P) * a.D * 2;
+    uint32_t h_off = 0;
+    auto aim = [&]() __attribute__((always_inline)) {
+      const int64_t row = static_cast<int64_t>(uniform(plan.list[l_j])) * a.H + blockIdx.x * 16;
+      pw = a.wd + row * row_bytes;
+      if constexpr (F != kW16) q = static_cast<const uint8_t*>(a.sd) + row * (F == kWFp8 ? 4 : a.D / 32);
+      h_off = static_cast<uint32_t>(pair[l_j * kRows + lr] * a.D + lg * EL) * (hw_fp32<DT, F>() ? 4 : 2);
+    };
+    DownSlot<DT, F> ring[S];
+    auto load = [&](DownSlot<DT, F>& s) __attribute__((always_inline)) {
+      const int64_t c = l_c;
+      s.w = *reinterpret_cast<const u32x4*>(pw + c * 64 + w_off);
+      if constexpr (hw_fp32<DT, F>()) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) s.h[i] = *reinterpret_cast<const u32x4*>(a.hw + c * (16 * EL) + h_off + 16 * i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+          s.h[i] = *reinterpret_cast<const u32x4*>(a.hw + c * (8 * EL) + h_off + 16 * i);
+          s.h[NX + i] = *reinterpret_cast<const u32x4*>(low + c * (8 * EL) + h_off + 16 * i);
+        }
+      }
+      if constexpr (F == kWFp8) s.s = *reinterpret_cast<const uint32_t*>(q + s_off);
+      else if constexpr (F == kWMx) s.s = (q + c * 4)[s_off];
+      if (--l_left > 0) {
+        if (++l_c == chunks) {
+          l_c = 0;
+          ++l_j;
+          aim();
+        }
+      }          // else: the last chunk is read again (in bounds, never used)
+    };
+    aim();
+#pragma unroll
+    for (int s = 0; s < S; ++s) load(ring[s]);
+    int j = u0 / pairs, c = 2 * (u0 % pairs), left = 2 * (u1 - u0);
+    auto step = [&](auto U) __attribute__((always_inline)) {
+      constexpr int s = decltype(U)::value;
+      if constexpr (hw_fp32<DT, F>()) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t w = ring[s].w[i >> 1];
+          acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(ring[s].h[i >> 2][i & 3]),
+                                                     f16_to_float((i & 1) ? (w >> 16) : (w & 0xffffu)), acc, 0, 0, 0);
+        }
+      } else {
+        u32x4 w[NX];
+        decode<kBF16, F>(ring[s].w, ring[s].s, w);
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+          acc = mfma16<kBF16>(ring[s].h[i], w[i], acc);
+          acc = mfma16<kBF16>(ring[s].h[NX + i], w[i], acc);
+        }
+      }
+      const float scale = F == kWFp8 ? __uint_as_float(ring[s].s) : 1.0f;
+      load(ring[s]);
+      --left;
+      if (++c == chunks || left == 0) {      // this wave's part of expert j is complete
+        c = 0;
+        const uint32_t m = static_cast<uint32_t>(uniform(plan.mask[plan.list[j]])) >> (lg * 4);
+        ++j;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] += (m >> i) & 1 ? acc[i] * scale : 0.0f;
+        acc = f32x4{};
+      }
+    };
+    const int mine = left;
+    for (int i = 0; i < mine / S; ++i) static_for<S>(step);
+    static_for<S>([&](auto U) __attribute__((always_inline)) {
+      if (decltype(U)::value < mine % S) step(U);
+    });
+  }
+  red[wave][lane] = sum;
+  __syncthreads();
+  if (tid < 256) {                       // register tid / 64 of lane tid % 64
+    const int t = lg * 4 + wave;
+    float v = 0.0f;
+    for (int w = 0; w < NW; ++w) v += reinterpret_cast<const float*>(&red[w][lane])[wave];
+    if (t < a.T) {
+      static_cast<uint16_t*>(a.y)[static_cast<int64_t>(t) * a.H + col] = static_cast<uint16_t>(from_float<DT>(v));
+    }
+  }
+}
+
+// ----------------------------------------------------------------- launch --
+
+template <int DT>
+void launch_logits(const FewProblem& p, hipStream_t st) {
+  const uint16_t* x = static_cast<const uint16_t*>(p.x);
+  auto go = [&](auto TT) {
+    hipLaunchKernelGGL((few_logits_kernel<DT, decltype(TT)::value>), dim3(p.E), dim3(256), 0, st, x,
+                       p.w_router, p.bias, p.T, p.H, p.E, p.logits);
+  };
+  if (p.T == 1) go(int_c<1>{});
+  else if (p.T == 2) go(int_c<2>{});
+  else if (p.T <= 4) go(int_c<4>{});
+  else if (p.T <= 8) go(int_c<8>{});
+  else go(int_c<16>{});
+}
+
+template <int DT, int F>
+hipError_t launch_typed(const FewProblem& p, hipStream_t st) {
+  FewArgs a{p.x, static_cast<const uint8_t*>(p.wg), static_cast<const uint8_t*>(p.wu),
+            static_cast<const uint8_t*>(p.wd), p.sg, p.su, p.sd, nullptr, p.ids, p.weights,
+            static_cast<uint8_t*>(p.hw), p.y, p.T, p.H, p.D, p.E, p.K, p.renorm};
+  if (p.w_router) {
+    launch_logits<DT>(p, st);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    a.logits = p.logits;
+  }
+  // Items of the most experts there can be; four workgroups fit a CU.
+  const int most = p.T * p.K < p.E ? p.T * p.K : p.E;
+  const int64_t items = static_cast<int64_t>(most) * (p.D / 16);
+  const int grid = static_cast<int>(items < 1024 ? items : 1024);
+  hipLaunchKernelGGL((few_gate_up_kernel<DT, F>), dim3(grid), dim3(kGateUpThreads), 0, st, a);
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  const int cols = p.H / 16;
+  if (cols <= 256) {
+    hipLaunchKernelGGL((few_down_kernel<DT, F, 16>), dim3(cols), dim3(1024), 0, st, a);
+  } else {
+    hipLaunchKernelGGL((few_down_kernel<DT, F, 8>), dim3(cols), dim3(512), 0, st, a);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_few(const FewProblem& p, hipStream_t st) {
+  switch (p.fmt) {
+    case kFewW16: return p.dtype == kBF16 ? launch_typed<kBF16, kW16>(p, st) : launch_typed<kF16, kW16>(p, st);
+    case kFewFp8: return p.dtype == kBF16 ? launch_typed<kBF16, kWFp8>(p, st) : launch_typed<kF16, kWFp8>(p, st);
+    default: return p.dtype == kBF16 ? launch_typed<kBF16, kWMx>(p, st) : launch_typed<kF16, kWMx>(p, st);
+  }
+}
+
+}  // namespace moe

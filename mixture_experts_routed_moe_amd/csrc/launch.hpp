@@ -132,4 +132,21 @@ struct NormProblem {
 };
 hipError_t launch_block_norm(const NormProblem& p, hipStream_t stream);
 
+// A whole layer for at most 16 tokens (few.hip).
+constexpr int kFewW16 = 0, kFewFp8 = 1, kFewMx = 2;
+struct FewProblem {
+  const void* x;            // [T, H] of dtype (kF16 / kBF16)
+  const float* w_router;    // [E, H], or nullptr: ids and weights are given
+  const float* bias;        // [E] or nullptr
+  const void *wg, *wu, *wd; // expert weights in format fmt
+  const void *sg, *su, *sd; // FP8: fp32 row scales; MXFP4: E8M0 block scales
+  int T, H, D, E, K, renorm, dtype, fmt;
+  int32_t* ids;             // [T, K], written when w_router is given
+  float* weights;           // [T, K]; nullptr (given routing) = ones
+  float* logits;            // workspace [T, E]
+  void* hw;                 // workspace [T * K, D], 4 bytes each
+  void* y;
+};
+hipError_t launch_few(const FewProblem& p, hipStream_t stream);
+
 }  // namespace moe

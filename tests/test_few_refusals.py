@@ -1,0 +1,50 @@
+"""What the layer for few tokens refuses, on the host and before any launch
+(addresses here are never dereferenced)."""
+import pytest
+
+from mixture_experts_routed_moe_amd import _lib
+
+A = 1 << 20
+NULL, SHAPE, DTYPE, UNSUPPORTED, WORKSPACE = 1, 2, 3, 4, 5
+
+
+def _few(fmt="", x=A, router=A, bias=None, w=A, s=A, T=4, H=256, D=256, E=8, K=2, renorm=1, dtype=1,
+         ids=A, weights=A, ws=A, ws_bytes=None, y=A):
+    L = _lib.lib()
+    n = L.moe_few_workspace_bytes(T, K, E, D) if ws_bytes is None else ws_bytes
+    scales = () if fmt == "" else (s, s, s)
+    return getattr(L, "moe_layer_few" + fmt)(x, router, bias, w, w, w, *scales, T, H, D, E, K, renorm, dtype,
+                                             ids, weights, ws, n, y, None)
+
+
+@pytest.mark.parametrize("fmt", ["", "_w8", "_mx"])
+@pytest.mark.parametrize("bad, status", [
+    (dict(x=None), NULL), (dict(w=None), NULL), (dict(ids=None), NULL), (dict(ws=None, ws_bytes=1 << 30), NULL),
+    (dict(y=None), NULL), (dict(weights=None), NULL), (dict(router=None, bias=A), NULL),
+    (dict(T=-1), SHAPE), (dict(T=17), UNSUPPORTED), (dict(H=0), SHAPE), (dict(H=320), SHAPE),
+    (dict(H=1 << 25), SHAPE), (dict(D=0), SHAPE), (dict(D=192), SHAPE), (dict(E=0), SHAPE), (dict(E=1025), SHAPE),
+    (dict(K=0), SHAPE), (dict(K=65, E=100), SHAPE), (dict(K=9), SHAPE), (dict(T=16, K=64, E=64, D=1 << 20), SHAPE),
+    (dict(dtype=2), DTYPE), (dict(dtype=7), DTYPE),
+    (dict(x=A + 2), SHAPE), (dict(w=A + 8), SHAPE), (dict(router=A + 4), SHAPE),
+    (dict(ws_bytes=0), WORKSPACE), (dict(ws=A + 16), WORKSPACE),
+])
+def test_refusals(fmt, bad, status):
+    assert _few(fmt, **bad) == status
+    assert _lib.lib().moe_last_error()
+
+
+def test_scales_and_block_rows():
+    assert _few("_w8", s=None) == NULL and _few("_mx", s=None) == NULL
+    assert _few("_mx", D=128) == SHAPE
+
+
+def test_workspace_bytes():
+    f = _lib.lib().moe_few_workspace_bytes
+    assert f(16, 8, 256, 2048) == 16 * 256 * 4 + 16 * 8 * 2048 * 4
+    assert f(17, 8, 256, 2048) == 0 and f(1, 8, 256, 100) == 0 and f(1, 0, 256, 128) == 0
+    n = f(4, 2, 8, 256)
+    assert _few(ws_bytes=n - 1) == WORKSPACE
+
+
+def test_no_tokens_launch_nothing():
+    assert _few(T=0) == 0 and _few("_mx", T=0, router=None) == 0
