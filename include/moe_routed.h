@@ -466,6 +466,34 @@ moe_status moe_routed_forward_mx(const void* x, const uint8_t* w_gate, const uin
                                  int dtype, void* workspace, size_t workspace_bytes, void* y,
                                  void* stream);
 
+/* MXFP4 experts on both sides (the block-scaled mode with E2M1 elements for
+ * the activations too): weights as moe_expert_gate_up_mx takes them, MXFP4
+ * activations (codes [rows, n/2], E8M0 scales [rows, n/32], the form of
+ * moe_quantize_mx_rows with MOE_MX_FP4 or of a norm with MOE_QUANT_MXFP4).
+ *   moe_expert_gate_up_mx4: xq [T, H/2], xs [T, H/32] (token order) ->
+ *     hq [P, D/2], hs [P, D/32] (sorted order) = MXFP4(SiLU(g) * u), quantised
+ *     from the fp32 sums (there is no 16-bit h);
+ *   moe_expert_down_mx4: expert_out [P, H] = R(hq . Wd), of dtype MOE_F16 or
+ *     MOE_BF16. Rows >= n_valid are not written by either.
+ * moe_routed_forward_mx4: x (16-bit) -> MXFP4; gate/up; down;
+ * moe_reduce_fused. Workspace (moe_forward_mx4_workspace_bytes, 256-byte
+ * aligned): expert_out, then xq, xs, hq, hs, each at the next 256-byte
+ * boundary. H % 256 == 0, D % 256 == 0, T * H <= 2^32; every array on
+ * a 16-byte boundary. Errors as the 16-bit calls. */
+moe_status moe_expert_gate_up_mx4(const uint8_t* xq, const uint8_t* xs, const uint8_t* w_gate,
+                                  const uint8_t* w_up, const uint8_t* s_gate, const uint8_t* s_up,
+                                  const moe_tables* tables, int H, int D, uint8_t* hq, uint8_t* hs,
+                                  void* stream);
+moe_status moe_expert_down_mx4(const uint8_t* hq, const uint8_t* hs, const uint8_t* w_down,
+                               const uint8_t* s_down, const moe_tables* tables, int H, int D,
+                               int dtype, void* expert_out, void* stream);
+size_t moe_forward_mx4_workspace_bytes(int T, int K, int H, int D, int dtype);
+moe_status moe_routed_forward_mx4(const void* x, const uint8_t* w_gate, const uint8_t* w_up,
+                                  const uint8_t* w_down, const uint8_t* s_gate,
+                                  const uint8_t* s_up, const uint8_t* s_down,
+                                  const moe_tables* tables, int H, int D, int dtype,
+                                  void* workspace, size_t workspace_bytes, void* y, void* stream);
+
 /* Step 3: top-k weighted reduce back to token order ([C] sections 1-2):
  *   y[t, :] = R_out( sum over k = 0..K-1 ascending with pos[t,k] >= 0 of
  *                    w[t,k] * expert_out[pos[t,k], :] )

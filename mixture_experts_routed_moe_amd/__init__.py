@@ -31,7 +31,8 @@ __all__ = ["MoeError", "MoeTables", "FP8Weights", "default_block_m", "moe_gate",
            "moe_routed_forward_w4a8", "MX_FP8", "MX_FP4", "MXWeights", "quantize_mx_rows",
            "quantize_mx_weights", "moe_expert_gate_up_mx", "moe_expert_down_mx",
            "forward_mx_workspace", "moe_routed_forward_mx", "moe_block_norm", "moe_reduce_norm",
-           "few_workspace", "moe_layer_few", "moe_layer_few_routed"]
+           "few_workspace", "moe_layer_few", "moe_layer_few_routed", "moe_expert_gate_up_mx4",
+           "moe_expert_down_mx4", "forward_mx4_workspace", "moe_routed_forward_mx4"]
 
 MX_FP8, MX_FP4 = 0, 4
 
@@ -1187,3 +1188,105 @@ def moe_layer_few_routed(x, topk_ids, topk_weights, w_gate, w_up, w_down, y=None
             raise MoeError(MOE_ERR_SHAPE, "topk_weights must be %s" % (tuple(topk_ids.shape),))
     return _few(x, None, None, w_gate, w_up, w_down, topk_ids.shape[1], False, topk_ids,
                 topk_weights, workspace, y)
+
+
+def _check_mx(weights, device):
+    for n, w in weights:
+        if not isinstance(w, MXWeights):
+            raise MoeError(MOE_ERR_DTYPE, "%s must be MXWeights (got %s)" % (n, type(w).__name__))
+        _check_tensor(w.packed, n, torch.uint8, 3, device)
+
+
+def _check_mxfp4_rows(codes, scales, name, rows, device):
+    """Checks MXFP4 activation rows; returns their length."""
+    _check_tensor(codes, name + "q", torch.uint8, 2, device)
+    _check_tensor(scales, name + "s", torch.uint8, 2, device)
+    n = 2 * codes.shape[1]
+    if codes.shape[0] != rows or tuple(scales.shape) != (rows, n // 32):
+        raise MoeError(MOE_ERR_SHAPE, "%sq must be [%d, n/2] and %ss [%d, n/32] (got %s, %s)"
+                       % (name, rows, name, rows, tuple(codes.shape), tuple(scales.shape)))
+    return n
+
+
+def moe_expert_gate_up_mx4(xq, xs, w_gate, w_up, tables, hq=None, hs=None):
+    """Step 2a with MXFP4 on both sides: xq [T, H/2], xs [T, H/32] (as
+    quantize_mx_rows with MX_FP4 or a norm with quant="mxfp4" gives them)
+    against MXWeights [E, D, H]. Returns the hidden rows in MXFP4, quantised
+    from the fp32 sums: hq [T*K, D/2], hs [T*K, D/32]."""
+    dev = tables.device if tables.device.index is not None else xq.device
+    _check_mx((("w_gate", w_gate), ("w_up", w_up)), dev)
+    H = _check_mxfp4_rows(xq, xs, "x", tables.T, dev)
+    E, D = tables.E, w_gate.shape[1]
+    if tuple(w_gate.shape) != (E, D, H) or tuple(w_up.shape) != (E, D, H):
+        raise MoeError(MOE_ERR_SHAPE, "w_gate and w_up must be [%d, D, %d] (got %s, %s)"
+                       % (E, H, tuple(w_gate.shape), tuple(w_up.shape)))
+    P = tables.T * tables.K
+    hq = _output(hq, "hq", (P, D // 2), torch.uint8, dev)
+    hs = _output(hs, "hs", (P, D // 32), torch.uint8, dev)
+    with _on(dev):
+        check(lib().moe_expert_gate_up_mx4(_ptr(xq), _ptr(xs), _ptr(w_gate.packed), _ptr(w_up.packed),
+                                           _ptr(w_gate.scales), _ptr(w_up.scales), tables.ref, H, D,
+                                           _ptr(hq), _ptr(hs), _stream(dev)))
+    return hq, hs
+
+
+def moe_expert_down_mx4(hq, hs, w_down, tables, dtype=torch.bfloat16, expert_out=None):
+    """Step 2b with MXFP4 on both sides: hq [T*K, D/2], hs [T*K, D/32] against
+    MXWeights [E, H, D]; expert_out [T*K, H] of dtype."""
+    dev = tables.device if tables.device.index is not None else hq.device
+    _check_mx((("w_down", w_down),), dev)
+    if dtype not in (torch.float16, torch.bfloat16):
+        raise MoeError(MOE_ERR_DTYPE, "expert_out must be float16 or bfloat16 (got %s)" % dtype)
+    P = tables.T * tables.K
+    D = _check_mxfp4_rows(hq, hs, "h", P, dev)
+    H = w_down.shape[1]
+    if tuple(w_down.shape) != (tables.E, H, D):
+        raise MoeError(MOE_ERR_SHAPE, "w_down must be [%d, H, %d] (got %s)" % (tables.E, D, tuple(w_down.shape)))
+    expert_out = _output(expert_out, "expert_out", (P, H), dtype, dev)
+    with _on(dev):
+        check(lib().moe_expert_down_mx4(_ptr(hq), _ptr(hs), _ptr(w_down.packed), _ptr(w_down.scales),
+                                        tables.ref, H, D, _DTYPE_CODE[dtype], _ptr(expert_out),
+                                        _stream(dev)))
+    return expert_out
+
+
+def forward_mx4_workspace(tables, H, D, dtype):
+    """A workspace for moe_routed_forward_mx4 and views of its buffers:
+    (ws, expert_out, xq, xs, hq, hs)."""
+    T, P = tables.T, tables.T * tables.K
+    nbytes = lib().moe_forward_mx4_workspace_bytes(T, tables.K, H, D, _DTYPE_CODE[dtype])
+    _require(nbytes > 0, MOE_ERR_SHAPE, "invalid workspace sizes")
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=tables.device)
+    views, off = [], 0
+    for rows, cols in ((P, 2 * H), (T, H // 2), (T, H // 32), (P, D // 2), (P, D // 32)):
+        views.append(ws[off:off + rows * cols].view(rows, cols))
+        off += (rows * cols + 255) // 256 * 256
+    return (ws, views[0].view(dtype), *views[1:])
+
+
+def moe_routed_forward_mx4(x, w_gate, w_up, w_down, tables, y=None, workspace=None):
+    """Steps 2-3 with MXFP4 on both sides (MXWeights; x 16-bit, quantised to
+    MXFP4 per token inside, the hidden rows in the gate/up epilogue): y [T, H]
+    of x.dtype. `workspace` from forward_mx4_workspace() (allocated here when
+    None)."""
+    _check_tensor(x, "x", None, 2)
+    dev = x.device
+    if x.dtype not in (torch.float16, torch.bfloat16):
+        raise MoeError(MOE_ERR_DTYPE, "MXFP4 experts take float16 or bfloat16 activations (got %s)" % x.dtype)
+    _check_mx((("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down)), dev)
+    T, H = x.shape
+    E, D = tables.E, w_gate.shape[1]
+    if (T != tables.T or tuple(w_gate.shape) != (E, D, H) or tuple(w_up.shape) != (E, D, H)
+            or tuple(w_down.shape) != (E, H, D)):
+        raise MoeError(MOE_ERR_SHAPE, "x must have %d rows, the weights be [%d, D, %d] twice and [%d, %d, D]"
+                       % (tables.T, E, H, E, H))
+    if workspace is None:
+        workspace = forward_mx4_workspace(tables, H, D, x.dtype)[0]
+    _check_tensor(workspace, "workspace", torch.uint8, 1, dev)
+    y = _output(y, "y", (T, H), x.dtype, dev)
+    with _on(dev):
+        check(lib().moe_routed_forward_mx4(_ptr(x), _ptr(w_gate.packed), _ptr(w_up.packed),
+                                           _ptr(w_down.packed), _ptr(w_gate.scales), _ptr(w_up.scales),
+                                           _ptr(w_down.scales), tables.ref, H, D, _DTYPE_CODE[x.dtype],
+                                           _ptr(workspace), workspace.numel(), _ptr(y), _stream(dev)))
+    return y

@@ -150,6 +150,15 @@ def lib():
         L.moe_layer_few_w8.restype = i32
         L.moe_layer_few_mx.argtypes = [vp] * 9 + few
         L.moe_layer_few_mx.restype = i32
+        L.moe_expert_gate_up_mx4.argtypes = [vp, vp, vp, vp, vp, vp, tp, i32, i32, vp, vp, vp]
+        L.moe_expert_gate_up_mx4.restype = i32
+        L.moe_expert_down_mx4.argtypes = [vp, vp, vp, vp, tp, i32, i32, i32, vp, vp]
+        L.moe_expert_down_mx4.restype = i32
+        L.moe_forward_mx4_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+        L.moe_forward_mx4_workspace_bytes.restype = sz
+        L.moe_routed_forward_mx4.argtypes = [vp, vp, vp, vp, vp, vp, vp, tp, i32, i32, i32, vp, sz,
+                                             vp, vp]
+        L.moe_routed_forward_mx4.restype = i32
         _lib = L
     return _lib
 

@@ -25,7 +25,7 @@ KERNEL_SOURCES = ["gate.hip", "dispatch.hip", "grouped_gemm.hip", "grouped_gemm_
                   "grouped_gemm_w8.hip", "grouped_gemm_w8a8.hip", "grouped_gemm_fused.hip",
                   "grouped_gemm_f32.hip", "quant.hip", "reduce.hip", "w4a8.hip", "mx.hip",
                   "noalloc.hip", "block_norm.hip",
-                  "few.hip"]
+                  "few.hip", "mx4.hip"]
 HOST_SOURCES = ["api.cpp"]
 
 

@@ -1034,4 +1034,109 @@ moe_status moe_layer_few_mx(const void* x, const float* w_router, const float* b
   return run_few(p, workspace, workspace_bytes, static_cast<hipStream_t>(stream), "moe_layer_few_mx launch");
 }
 
+static moe_status check_mx4(const moe_tables* t, int H, int D, int dtype,
+                            std::initializer_list<const void*> aligned) {
+  moe_status s = check_mx_shapes(t, H, D, dtype);
+  if (s != MOE_OK) return s;
+  if (static_cast<int64_t>(t->T) * H > (int64_t{1} << 32) || H > (1 << 24) || D > (1 << 24)) {
+    return fail(MOE_ERR_SHAPE, "T * H, H or D too large (T=%d, H=%d, D=%d)", t->T, H, D);
+  }
+  for (const void* p : aligned) {
+    if (reinterpret_cast<uintptr_t>(p) % 16 != 0) {
+      return fail(MOE_ERR_SHAPE, "MXFP4 codes, weights, scales and expert_out must be 16-byte aligned");
+    }
+  }
+  return MOE_OK;
+}
+
+moe_status moe_expert_gate_up_mx4(const uint8_t* xq, const uint8_t* xs, const uint8_t* w_gate,
+                                  const uint8_t* w_up, const uint8_t* s_gate, const uint8_t* s_up,
+                                  const moe_tables* tables, int H, int D, uint8_t* hq, uint8_t* hs,
+                                  void* stream) {
+  if (!xq || !xs || !w_gate || !w_up || !s_gate || !s_up || !hq || !hs) {
+    return fail(MOE_ERR_NULL, "xq, xs, the weights, their scales, hq and hs must not be NULL");
+  }
+  moe_status s = check_mx4(tables, H, D, MOE_BF16, {xq, xs, w_gate, w_up, s_gate, s_up, hq});
+  if (s != MOE_OK) return s;
+  moe::Mx4GemmProblem p{xq, xs, w_gate, w_up, s_gate, s_up, hq, hs, nullptr, D, H, MOE_BF16};
+  return hip_status(moe::launch_gate_up_mx4(p, *tables, static_cast<hipStream_t>(stream)),
+                    "moe_expert_gate_up_mx4 launch");
+}
+
+moe_status moe_expert_down_mx4(const uint8_t* hq, const uint8_t* hs, const uint8_t* w_down,
+                               const uint8_t* s_down, const moe_tables* tables, int H, int D,
+                               int dtype, void* expert_out, void* stream) {
+  if (!hq || !hs || !w_down || !s_down || !expert_out) {
+    return fail(MOE_ERR_NULL, "hq, hs, w_down, s_down and expert_out must not be NULL");
+  }
+  moe_status s = check_mx4(tables, H, D, dtype, {hq, hs, w_down, s_down, expert_out});
+  if (s != MOE_OK) return s;
+  moe::Mx4GemmProblem p{hq, hs, w_down, nullptr, s_down, nullptr, nullptr, nullptr, expert_out, H, D, dtype};
+  return hip_status(moe::launch_down_mx4(p, *tables, static_cast<hipStream_t>(stream)),
+                    "moe_expert_down_mx4 launch");
+}
+
+namespace {
+
+// Workspace of the MXFP4 forward: expert_out [P, H], xq [T, H/2], xs [T,
+// H/32], hq [P, D/2], hs [P, D/32], each 256-aligned.
+struct Mx4Layout {
+  size_t xq, xs, hq, hs, total;
+};
+
+Mx4Layout mx4_layout(int T, int K, int H, int D, int dtype) {
+  const size_t P = static_cast<size_t>(T) * K;
+  Mx4Layout L;
+  L.xq = align_up(P * H * dtype_bytes(dtype));
+  L.xs = L.xq + align_up(static_cast<size_t>(T) * (H / 2));
+  L.hq = L.xs + align_up(static_cast<size_t>(T) * (H / 32));
+  L.hs = L.hq + align_up(P * (D / 2));
+  L.total = L.hs + align_up(P * (D / 32));
+  return L;
+}
+
+}  // namespace
+
+size_t moe_forward_mx4_workspace_bytes(int T, int K, int H, int D, int dtype) {
+  if (T < 1 || K < 1 || H <= 0 || D <= 0 || !is_16bit(dtype)) return 0;
+  return mx4_layout(T, K, H, D, dtype).total;
+}
+
+moe_status moe_routed_forward_mx4(const void* x, const uint8_t* w_gate, const uint8_t* w_up,
+                                  const uint8_t* w_down, const uint8_t* s_gate,
+                                  const uint8_t* s_up, const uint8_t* s_down,
+                                  const moe_tables* tables, int H, int D, int dtype,
+                                  void* workspace, size_t workspace_bytes, void* y, void* stream) {
+  if (!x || !w_gate || !w_up || !w_down || !s_gate || !s_up || !s_down || !workspace || !y) {
+    return fail(MOE_ERR_NULL, "x, the weights, their scales, workspace and y must not be NULL");
+  }
+  moe_status s = check_mx4(tables, H, D, dtype, {x, w_gate, w_up, w_down, s_gate, s_up, s_down, y});
+  if (s != MOE_OK) return s;
+  const int T = tables->T, K = tables->K;
+  const Mx4Layout L = mx4_layout(T, K, H, D, dtype);
+  if (workspace_bytes < L.total) {
+    return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, L.total);
+  }
+  if (reinterpret_cast<uintptr_t>(workspace) % kAlign != 0) {
+    return fail(MOE_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  }
+  char* ws = static_cast<char*>(workspace);
+  uint8_t* xq = reinterpret_cast<uint8_t*>(ws + L.xq);
+  uint8_t* xs = reinterpret_cast<uint8_t*>(ws + L.xs);
+  uint8_t* hq = reinterpret_cast<uint8_t*>(ws + L.hq);
+  uint8_t* hs = reinterpret_cast<uint8_t*>(ws + L.hs);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  hipError_t err = moe::launch_quantize_mx_rows(x, T, H, dtype, MOE_MX_FP4, xq, xs, st);
+  if (err != hipSuccess) return hip_status(err, "moe_routed_forward_mx4 x quantisation launch");
+  moe::Mx4GemmProblem up{xq, xs, w_gate, w_up, s_gate, s_up, hq, hs, nullptr, D, H, dtype};
+  err = moe::launch_gate_up_mx4(up, *tables, st);
+  if (err != hipSuccess) return hip_status(err, "moe_routed_forward_mx4 gate/up launch");
+  moe::Mx4GemmProblem down{hq, hs, w_down, nullptr, s_down, nullptr, nullptr, nullptr, ws, H, D, dtype};
+  err = moe::launch_down_mx4(down, *tables, st);
+  if (err != hipSuccess) return hip_status(err, "moe_routed_forward_mx4 down launch");
+  err = moe::launch_reduce(ws, static_cast<int64_t>(T) * K, tables->token_topk_to_pos,
+                           tables->topk_weights, nullptr, nullptr, T, K, H, dtype, dtype, y, st);
+  return hip_status(err, "moe_routed_forward_mx4 reduce launch");
+}
+
 }  // extern "C"

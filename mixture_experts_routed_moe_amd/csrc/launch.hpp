@@ -149,4 +149,21 @@ struct FewProblem {
 };
 hipError_t launch_few(const FewProblem& p, hipStream_t stream);
 
+// MXFP4 on both sides (mx4.hip): activations a [rows, kd/2] with E8M0 block
+// scales as, weights b0 / b1 with s0 / s1; gate/up writes MXFP4 hidden rows
+// (hq, hs), down writes out in dtype (kF16 / kBF16).
+struct Mx4GemmProblem {
+  const uint8_t* a;
+  const uint8_t* as;
+  const uint8_t *b0, *b1;
+  const uint8_t *s0, *s1;
+  uint8_t *hq, *hs;
+  void* out;
+  int n;
+  int kd;
+  int dtype;
+};
+hipError_t launch_gate_up_mx4(const Mx4GemmProblem& p, const moe_tables& t, hipStream_t stream);
+hipError_t launch_down_mx4(const Mx4GemmProblem& p, const moe_tables& t, hipStream_t stream);
+
 }  // namespace moe
