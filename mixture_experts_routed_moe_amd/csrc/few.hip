@@ -28,9 +28,9 @@
 // Both GEMM kernels run one uninterrupted stream of chunks (64 bytes of each
 // of 16 weight rows = 1 KB a load) through a register ring that crosses item
 // and expert borders. MFMA rows of tokens that an expert does not serve read
-// a served token's row and are left out where sums are added up (a select:
-// nothing of an expert, not even a NaN, reaches a token that it does not
-// serve).
+// zeros through the buffer's bounds check (no memory is touched) and are left
+// out where sums are added up (a select: nothing of an expert, not even a
+// NaN, reaches a token that it does not serve).
 //
 // Precision: hw stays in 32 bits between the kernels. bf16, FP8 and MXFP4
 // weights meet it as a pair of bf16 (16 significant bits; a single bf16 would
@@ -76,15 +76,18 @@ struct FewArgs {
 
 // ---------------------------------------------------------------- router --
 
-// Logits of expert blockIdx.x for TT >= T tokens: every thread strides over
-// the row four elements at a time, fp64 sums go lane -> wave -> workgroup.
+// Logits of expert blockIdx.x for tokens TT * blockIdx.y and on: every thread
+// strides over the row four elements at a time, fp64 sums go lane -> wave ->
+// workgroup.
 template <int DT, int TT>
 __global__ __launch_bounds__(256) void few_logits_kernel(const uint16_t* __restrict__ x,
                                                          const float* __restrict__ wr,
                                                          const float* __restrict__ bias, int T,
                                                          int H, int E, float* __restrict__ logits) {
   __shared__ double part[4][TT];
-  const int e = blockIdx.x, tid = threadIdx.x;
+  const int e = blockIdx.x, tid = threadIdx.x, t0 = blockIdx.y * TT;
+  x += static_cast<int64_t>(t0) * H;
+  T -= t0;
   double acc[TT];
 #pragma unroll
   for (int t = 0; t < TT; ++t) acc[t] = 0.0;
@@ -109,10 +112,10 @@ __global__ __launch_bounds__(256) void few_logits_kernel(const uint16_t* __restr
     if ((tid & 63) == 0) part[tid >> 6][t] = acc[t];
   }
   __syncthreads();
-  if (tid < T) {
+  if (tid < T && tid < TT) {
     double s = part[0][tid] + part[1][tid] + part[2][tid] + part[3][tid];
     if (bias) s += static_cast<double>(bias[e]);
-    logits[static_cast<int64_t>(tid) * E + e] = static_cast<float>(s);
+    logits[static_cast<int64_t>(t0 + tid) * E + e] = static_cast<float>(s);
   }
 }
 
@@ -239,6 +242,16 @@ __device__ __forceinline__ void build_plan(Plan& s, int P, int K, int E, int tid
 }
 
 // --------------------------------------------------------------- operands --
+
+// 16 bytes at byte `lane_off + wave_off` of a buffer; zeros, without touching
+// memory, where the sum is past its size (kNoRow: rows that do not exist).
+constexpr uint32_t kNoRow = 0x80000000u;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, static_cast<int>(bytes), 0x00027000);
+}
+__device__ __forceinline__ u32x4 buffer_load16(__amdgpu_buffer_rsrc_t b, uint32_t lane_off, int wave_off) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, static_cast<int>(lane_off), wave_off, 0));
+}
 
 // A value that is the same in all lanes, in a scalar register.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -380,17 +393,16 @@ __global__ __launch_bounds__(kGateUpThreads, 4) void few_gate_up_kernel(FewArgs 
       qu = static_cast<const uint8_t*>(a.su) + row * (F == kWFp8 ? 4 : blocks);
     }
     const uint32_t m = static_cast<uint32_t>(uniform(static_cast<int>(plan.mask[e])));
-    const int t = (m >> lr) & 1 ? lr : __builtin_ctz(m);
-    x_off = static_cast<uint32_t>(t * a.H + lg * EL) * 2;
+    x_off = (m >> lr) & 1 ? static_cast<uint32_t>(lr * a.H + lg * EL) * 2 : kNoRow;
   };
+  const __amdgpu_buffer_rsrc_t xb = buffer_of(a.x, static_cast<int64_t>(a.T) * a.H * 2);
   GateUpSlot<F> ring[S];
   auto load = [&](GateUpSlot<F>& s) __attribute__((always_inline)) {
     const int64_t c = 8 * (l_c >> 1) + 2 * wave + (l_c & 1);
     s.g = *reinterpret_cast<const u32x4*>(pg + c * 64 + w_off);
     s.u = *reinterpret_cast<const u32x4*>(pu + c * 64 + w_off);
-    const uint8_t* px = static_cast<const uint8_t*>(a.x) + c * (8 * EL);
 #pragma unroll
-    for (int i = 0; i < NX; ++i) s.x[i] = *reinterpret_cast<const u32x4*>(px + x_off + 16 * i);
+    for (int i = 0; i < NX; ++i) s.x[i] = buffer_load16(xb, x_off + 16 * i, static_cast<int>(c) * (8 * EL));
     if constexpr (F == kWFp8) {
       s.sg = *reinterpret_cast<const uint32_t*>(qg + s_off);
       s.su = *reinterpret_cast<const uint32_t*>(qu + s_off);
@@ -539,10 +551,12 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs a) {
   for (int i = tid; i < plan.count * kRows; i += 64 * NW) {
     const int e = plan.list[i / kRows];
     const uint32_t m = plan.mask[e];
-    const int t = (m >> (i % kRows)) & 1 ? i % kRows : __builtin_ctz(m);
-    int p = 0;
-    for (int k = a.K - 1; k >= 0; --k) {
-      if (plan.sid[t * a.K + k] == e) p = t * a.K + k;
+    const int t = i % kRows;
+    int p = kMaxP;                                  // not one of this expert's tokens
+    if ((m >> t) & 1) {
+      for (int k = a.K - 1; k >= 0; --k) {
+        if (plan.sid[t * a.K + k] == e) p = t * a.K + k;
+      }
     }
     pair[i] = static_cast<uint16_t>(p);
   }
@@ -562,13 +576,16 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs a) {
     const uint8_t *pw = nullptr, *q = nullptr;
     const uint32_t w_off = static_cast<uint32_t>(lr * row_bytes) + lg * 16;
     const uint32_t s_off = F == kWFp8 ? lr * 4 : static_cast<uint32_t>(lr * (a.D / 32)) + lg;
-    const uint8_t* low = a.hw + static_cast<int64_t>(P) * a.D * 2;
+    const int64_t half = static_cast<int64_t>(P) * a.D * 2;
+    const __amdgpu_buffer_rsrc_t hb = buffer_of(a.hw, hw_fp32<DT, F>() ? 2 * half : half);
+    const __amdgpu_buffer_rsrc_t lb = buffer_of(a.hw + half, half);
     uint32_t h_off = 0;
     auto aim = [&]() __attribute__((always_inline)) {
       const int64_t row = static_cast<int64_t>(uniform(plan.list[l_j])) * a.H + blockIdx.x * 16;
       pw = a.wd + row * row_bytes;
       if constexpr (F != kW16) q = static_cast<const uint8_t*>(a.sd) + row * (F == kWFp8 ? 4 : a.D / 32);
-      h_off = static_cast<uint32_t>(pair[l_j * kRows + lr] * a.D + lg * EL) * (hw_fp32<DT, F>() ? 4 : 2);
+      const int p = pair[l_j * kRows + lr];
+      h_off = p < kMaxP ? static_cast<uint32_t>(p * a.D + lg * EL) * (hw_fp32<DT, F>() ? 4 : 2) : kNoRow;
     };
     DownSlot<DT, F> ring[S];
     auto load = [&](DownSlot<DT, F>& s) __attribute__((always_inline)) {
@@ -576,12 +593,12 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs a) {
       s.w = *reinterpret_cast<const u32x4*>(pw + c * 64 + w_off);
       if constexpr (hw_fp32<DT, F>()) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) s.h[i] = *reinterpret_cast<const u32x4*>(a.hw + c * (16 * EL) + h_off + 16 * i);
+        for (int i = 0; i < 2; ++i) s.h[i] = buffer_load16(hb, h_off + 16 * i, l_c * (16 * EL));
       } else {
 #pragma unroll
         for (int i = 0; i < NX; ++i) {
-          s.h[i] = *reinterpret_cast<const u32x4*>(a.hw + c * (8 * EL) + h_off + 16 * i);
-          s.h[NX + i] = *reinterpret_cast<const u32x4*>(low + c * (8 * EL) + h_off + 16 * i);
+          s.h[i] = buffer_load16(hb, h_off + 16 * i, l_c * (8 * EL));
+          s.h[NX + i] = buffer_load16(lb, h_off + 16 * i, l_c * (8 * EL));
         }
       }
       if constexpr (F == kWFp8) s.s = *reinterpret_cast<const uint32_t*>(q + s_off);
@@ -652,14 +669,13 @@ template <int DT>
 void launch_logits(const FewProblem& p, hipStream_t st) {
   const uint16_t* x = static_cast<const uint16_t*>(p.x);
   auto go = [&](auto TT) {
-    hipLaunchKernelGGL((few_logits_kernel<DT, decltype(TT)::value>), dim3(p.E), dim3(256), 0, st, x,
+    constexpr int tt = decltype(TT)::value;
+    hipLaunchKernelGGL((few_logits_kernel<DT, tt>), dim3(p.E, (p.T + tt - 1) / tt), dim3(256), 0, st, x,
                        p.w_router, p.bias, p.T, p.H, p.E, p.logits);
   };
   if (p.T == 1) go(int_c<1>{});
   else if (p.T == 2) go(int_c<2>{});
-  else if (p.T <= 4) go(int_c<4>{});
-  else if (p.T <= 8) go(int_c<8>{});
-  else go(int_c<16>{});
+  else go(int_c<4>{});
 }
 
 template <int DT, int F>
