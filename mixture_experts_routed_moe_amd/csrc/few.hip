@@ -326,17 +326,18 @@ constexpr bool hw_fp32() {
   return DT == kF16 && F == kW16;
 }
 
-// One chunk of a wave: 64 bytes of 16 gate and 16 up rows, the tokens' x.
+// One step of a wave: a pair of chunks (both halves of the 128-byte lines of 16
+// gate and 16 up rows) and the tokens' x.
 template <int F>
 struct GateUpSlot {
-  u32x4 g, u;
-  u32x4 x[lane_elems<F>() / 8];
-  uint32_t sg, su;              // FP8: the rows' fp32 scales; MXFP4: E8M0 bytes
+  u32x4 g[2], u[2];
+  u32x4 x[2][lane_elems<F>() / 8];
+  uint32_t sg[2], su[2];        // FP8: the rows' fp32 scales (in [0]); MXFP4: E8M0 bytes
 };
 
 template <int DT, int F>
 __global__ __launch_bounds__(kGateUpThreads, 4) void few_gate_up_kernel(FewArgs a) {
-  constexpr int EL = lane_elems<F>(), NX = EL / 8, S = F == kW16 ? 8 : (F == kWFp8 ? 5 : 3);
+  constexpr int EL = lane_elems<F>(), NX = EL / 8, S = F == kW16 ? 4 : 2;
   __shared__ Plan plan;
   __shared__ float sw[kMaxP];
   __shared__ f32x4 red[2][4][2][64];
@@ -370,9 +371,9 @@ __global__ __launch_bounds__(kGateUpThreads, 4) void few_gate_up_kernel(FewArgs 
   const int tiles = a.D / 16;
   const int items = plan.count * tiles;
   if (static_cast<int>(blockIdx.x) >= items) return;
-  // This wave's chunks of every item: pairs (128 bytes a row) wave, wave + 4, ...
+  // This wave's steps of every item: pairs of chunks (128 bytes a row) wave, wave + 4, ...
   const int pairs = a.H / (8 * EL);
-  const int n = 2 * ((pairs - wave + 3) / 4);
+  const int n = (pairs - wave + 3) / 4;
   const int64_t row_bytes = static_cast<int64_t>(a.H / EL) * 16;
   const int64_t blocks = a.H / 32;
 
@@ -398,20 +399,31 @@ __global__ __launch_bounds__(kGateUpThreads, 4) void few_gate_up_kernel(FewArgs 
   const __amdgpu_buffer_rsrc_t xb = buffer_of(a.x, static_cast<int64_t>(a.T) * a.H * 2);
   GateUpSlot<F> ring[S];
   auto load = [&](GateUpSlot<F>& s) __attribute__((always_inline)) {
-    const int64_t c = 8 * (l_c >> 1) + 2 * wave + (l_c & 1);
-    s.g = *reinterpret_cast<const u32x4*>(pg + c * 64 + w_off);
-    s.u = *reinterpret_cast<const u32x4*>(pu + c * 64 + w_off);
+    // Both halves of a line right after one another: with other loads between
+    // them the second one stalls the first-level cache on the pending line.
+    const int64_t c = 4 * l_c + wave;
+    const uint8_t *g = pg + c * 128, *u = pu + c * 128;
+    s.g[0] = *reinterpret_cast<const u32x4*>(g + w_off);
+    s.g[1] = *reinterpret_cast<const u32x4*>(g + w_off + 64);
+    s.u[0] = *reinterpret_cast<const u32x4*>(u + w_off);
+    s.u[1] = *reinterpret_cast<const u32x4*>(u + w_off + 64);
 #pragma unroll
-    for (int i = 0; i < NX; ++i) s.x[i] = buffer_load16(xb, x_off + 16 * i, static_cast<int>(c) * (8 * EL));
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int i = 0; i < NX; ++i) {
+        s.x[k][i] = buffer_load16(xb, x_off + 16 * i, static_cast<int>(c) * (16 * EL) + k * (8 * EL));
+      }
+      if constexpr (F == kWMx) {
+        s.sg[k] = (qg + c * 8 + k * 4)[s_off];
+        s.su[k] = (qu + c * 8 + k * 4)[s_off];
+      }
+    }
     if constexpr (F == kWFp8) {
-      s.sg = *reinterpret_cast<const uint32_t*>(qg + s_off);
-      s.su = *reinterpret_cast<const uint32_t*>(qu + s_off);
-    } else if constexpr (F == kWMx) {
-      s.sg = (qg + c * 4)[s_off];
-      s.su = (qu + c * 4)[s_off];
+      s.sg[0] = *reinterpret_cast<const uint32_t*>(qg + s_off);
+      s.su[0] = *reinterpret_cast<const uint32_t*>(qu + s_off);
     }
     if (++l_c == n) {
-      // past the last item the last chunk is read again (in bounds, never used)
+      // past the last item the last pair is read again (in bounds, never used)
       if (l_item + static_cast<int>(gridDim.x) < items) {
         l_item += gridDim.x;
         l_c = 0;
@@ -489,26 +501,29 @@ __global__ __launch_bounds__(kGateUpThreads, 4) void few_gate_up_kernel(FewArgs 
   int c = 0;
   auto step = [&](auto U) __attribute__((always_inline)) {
     constexpr int s = decltype(U)::value;
-    u32x4 wg[NX], wu[NX];
-    decode<DT, F>(ring[s].g, ring[s].sg, wg);
-    decode<DT, F>(ring[s].u, ring[s].su, wu);
 #pragma unroll
-    for (int i = 0; i < NX; ++i) {
-      if constexpr (F == kWMx && DT == kF16) {
-        u32x4 hi, lo;
-        split_f16x8(ring[s].x[i], hi, lo);
-        accg = mfma16<kBF16>(hi, wg[i], accg);
-        accu = mfma16<kBF16>(hi, wu[i], accu);
-        accg = mfma16<kBF16>(lo, wg[i], accg);
-        accu = mfma16<kBF16>(lo, wu[i], accu);
-      } else {
-        accg = mfma16<DT>(ring[s].x[i], wg[i], accg);
-        accu = mfma16<DT>(ring[s].x[i], wu[i], accu);
+    for (int k = 0; k < 2; ++k) {
+      u32x4 wg[NX], wu[NX];
+      decode<DT, F>(ring[s].g[k], ring[s].sg[k], wg);
+      decode<DT, F>(ring[s].u[k], ring[s].su[k], wu);
+#pragma unroll
+      for (int i = 0; i < NX; ++i) {
+        if constexpr (F == kWMx && DT == kF16) {
+          u32x4 hi, lo;
+          split_f16x8(ring[s].x[k][i], hi, lo);
+          accg = mfma16<kBF16>(hi, wg[i], accg);
+          accu = mfma16<kBF16>(hi, wu[i], accu);
+          accg = mfma16<kBF16>(lo, wg[i], accg);
+          accu = mfma16<kBF16>(lo, wu[i], accu);
+        } else {
+          accg = mfma16<DT>(ring[s].x[k][i], wg[i], accg);
+          accu = mfma16<DT>(ring[s].x[k][i], wu[i], accu);
+        }
       }
     }
     if constexpr (F == kWFp8) {
-      scale_g = __uint_as_float(ring[s].sg);
-      scale_u = __uint_as_float(ring[s].su);
+      scale_g = __uint_as_float(ring[s].sg[0]);
+      scale_u = __uint_as_float(ring[s].su[0]);
     }
     load(ring[s]);
     if (++c == n) {
@@ -519,10 +534,10 @@ __global__ __launch_bounds__(kGateUpThreads, 4) void few_gate_up_kernel(FewArgs 
   // Whole turns of the ring without a condition around a load (one would make
   // the compiler wait for more loads than it has to), then the rest.
   const int mine = (items - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
-  const int chunks = mine * n;
-  for (int i = 0; i < chunks / S; ++i) static_for<S>(step);
+  const int steps = mine * n;
+  for (int i = 0; i < steps / S; ++i) static_for<S>(step);
   static_for<S>([&](auto U) __attribute__((always_inline)) {
-    if (decltype(U)::value < chunks % S) step(U);
+    if (decltype(U)::value < steps % S) step(U);
   });
 }
 
@@ -530,14 +545,14 @@ __global__ __launch_bounds__(kGateUpThreads, 4) void few_gate_up_kernel(FewArgs 
 
 template <int DT, int F>
 struct DownSlot {
-  u32x4 w;
-  u32x4 h[lane_elems<F>() / 4];   // hw: fp32 (8 elements in 2), or the high parts, then the low parts
-  uint32_t s;
+  u32x4 w[2];
+  u32x4 h[2][lane_elems<F>() / 4];   // hw: fp32 (8 elements in 2), or the high parts, then the low parts
+  uint32_t s[2];
 };
 
 template <int DT, int F, int NW>
 __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs a) {
-  constexpr int EL = lane_elems<F>(), NX = EL / 8, S = F == kW16 ? 8 : (F == kWFp8 ? 4 : 2);
+  constexpr int EL = lane_elems<F>(), NX = EL / 8, S = F == kW16 ? 4 : (F == kWFp8 ? 2 : 1);
   __shared__ Plan plan;
   __shared__ uint16_t pair[kMaxE * kRows];   // hw row of (distinct expert, token)
   __shared__ f32x4 red[NW][64];
@@ -568,11 +583,10 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs a) {
   const int total = plan.count * pairs;
   const int u0 = static_cast<int>(static_cast<int64_t>(total) * wave / NW);
   const int u1 = static_cast<int>(static_cast<int64_t>(total) * (wave + 1) / NW);
-  const int chunks = 2 * pairs;                     // of one expert
 
   f32x4 sum = {}, acc = {};
   if (u0 < u1) {
-    int l_j = u0 / pairs, l_c = 2 * (u0 % pairs), l_left = 2 * (u1 - u0);
+    int l_j = u0 / pairs, l_c = u0 % pairs, l_left = u1 - u0;
     const uint8_t *pw = nullptr, *q = nullptr;
     const uint32_t w_off = static_cast<uint32_t>(lr * row_bytes) + lg * 16;
     const uint32_t s_off = F == kWFp8 ? lr * 4 : static_cast<uint32_t>(lr * (a.D / 32)) + lg;
@@ -589,54 +603,61 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs a) {
     };
     DownSlot<DT, F> ring[S];
     auto load = [&](DownSlot<DT, F>& s) __attribute__((always_inline)) {
-      const int64_t c = l_c;
-      s.w = *reinterpret_cast<const u32x4*>(pw + c * 64 + w_off);
-      if constexpr (hw_fp32<DT, F>()) {
+      const uint8_t* w = pw + static_cast<int64_t>(l_c) * 128;
+      s.w[0] = *reinterpret_cast<const u32x4*>(w + w_off);
+      s.w[1] = *reinterpret_cast<const u32x4*>(w + w_off + 64);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) s.h[i] = buffer_load16(hb, h_off + 16 * i, l_c * (16 * EL));
-      } else {
+      for (int k = 0; k < 2; ++k) {
+        if constexpr (hw_fp32<DT, F>()) {
 #pragma unroll
-        for (int i = 0; i < NX; ++i) {
-          s.h[i] = buffer_load16(hb, h_off + 16 * i, l_c * (8 * EL));
-          s.h[NX + i] = buffer_load16(lb, h_off + 16 * i, l_c * (8 * EL));
+          for (int i = 0; i < 2; ++i) s.h[k][i] = buffer_load16(hb, h_off + 16 * i, (2 * l_c + k) * (16 * EL));
+        } else {
+#pragma unroll
+          for (int i = 0; i < NX; ++i) {
+            s.h[k][i] = buffer_load16(hb, h_off + 16 * i, (2 * l_c + k) * (8 * EL));
+            s.h[k][NX + i] = buffer_load16(lb, h_off + 16 * i, (2 * l_c + k) * (8 * EL));
+          }
         }
+        if constexpr (F == kWMx) s.s[k] = (q + l_c * 8 + k * 4)[s_off];
       }
-      if constexpr (F == kWFp8) s.s = *reinterpret_cast<const uint32_t*>(q + s_off);
-      else if constexpr (F == kWMx) s.s = (q + c * 4)[s_off];
+      if constexpr (F == kWFp8) s.s[0] = *reinterpret_cast<const uint32_t*>(q + s_off);
       if (--l_left > 0) {
-        if (++l_c == chunks) {
+        if (++l_c == pairs) {
           l_c = 0;
           ++l_j;
           aim();
         }
-      }          // else: the last chunk is read again (in bounds, never used)
+      }          // else: the last pair is read again (in bounds, never used)
     };
     aim();
 #pragma unroll
     for (int s = 0; s < S; ++s) load(ring[s]);
-    int j = u0 / pairs, c = 2 * (u0 % pairs), left = 2 * (u1 - u0);
+    int j = u0 / pairs, c = u0 % pairs, left = u1 - u0;
     auto step = [&](auto U) __attribute__((always_inline)) {
       constexpr int s = decltype(U)::value;
-      if constexpr (hw_fp32<DT, F>()) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t w = ring[s].w[i >> 1];
-          acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(ring[s].h[i >> 2][i & 3]),
-                                                     f16_to_float((i & 1) ? (w >> 16) : (w & 0xffffu)), acc, 0, 0, 0);
-        }
-      } else {
-        u32x4 w[NX];
-        decode<kBF16, F>(ring[s].w, ring[s].s, w);
+      for (int k = 0; k < 2; ++k) {
+        if constexpr (hw_fp32<DT, F>()) {
 #pragma unroll
-        for (int i = 0; i < NX; ++i) {
-          acc = mfma16<kBF16>(ring[s].h[i], w[i], acc);
-          acc = mfma16<kBF16>(ring[s].h[NX + i], w[i], acc);
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t w = ring[s].w[k][i >> 1];
+            acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(ring[s].h[k][i >> 2][i & 3]),
+                                                       f16_to_float((i & 1) ? (w >> 16) : (w & 0xffffu)), acc, 0, 0, 0);
+          }
+        } else {
+          u32x4 w[NX];
+          decode<kBF16, F>(ring[s].w[k], ring[s].s[k], w);
+#pragma unroll
+          for (int i = 0; i < NX; ++i) {
+            acc = mfma16<kBF16>(ring[s].h[k][i], w[i], acc);
+            acc = mfma16<kBF16>(ring[s].h[k][NX + i], w[i], acc);
+          }
         }
       }
-      const float scale = F == kWFp8 ? __uint_as_float(ring[s].s) : 1.0f;
+      const float scale = F == kWFp8 ? __uint_as_float(ring[s].s[0]) : 1.0f;
       load(ring[s]);
       --left;
-      if (++c == chunks || left == 0) {      // this wave's part of expert j is complete
+      if (++c == pairs || left == 0) {      // this wave's part of expert j is complete
         c = 0;
         const uint32_t m = static_cast<uint32_t>(uniform(plan.mask[plan.list[j]])) >> (lg * 4);
         ++j;
