@@ -609,9 +609,9 @@ moe_status moe_reduce_norm(const void* expert_out, int64_t rows,
  *   [T, E] at offset 0 and is written by every call (calls that overlap on
  *   two streams need one each).
  * Requires H % 256 == 0, D % 128 == 0 (_mx: D % 256 == 0), 1 <= E <= 1024,
- * 1 <= K <= 64 (and K <= E with w_router); x, weights, codes and MXFP4
- * codes on 16-byte boundaries. T == 0 returns MOE_OK and launches nothing.
- * Two kernels (three with w_router), no atomics on memory: results do not
+ * 1 <= K <= 64 (and K <= E with w_router); x, y, w_router, weights and
+ * MXFP4 scales on 16-byte boundaries. T == 0 returns MOE_OK and launches nothing.
+ * Three kernels (four with w_router), no atomics on memory: results do not
  * depend on the run. Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE,
  * MOE_ERR_UNSUPPORTED (T > MOE_FEW_MAX_TOKENS), MOE_ERR_WORKSPACE,
  * MOE_ERR_HIP. */

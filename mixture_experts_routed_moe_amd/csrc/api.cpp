@@ -957,7 +957,8 @@ static size_t few_logits_bytes(int T, int E) { return align_up(4 * static_cast<s
 size_t moe_few_workspace_bytes(int T, int K, int E, int D) {
   if (few_sizes(T, K, E, D) != MOE_OK) return 0;
   const int rows = T > 0 ? T : 1;
-  return few_logits_bytes(rows, E) + align_up(4 * static_cast<size_t>(rows) * K * D);
+  return few_logits_bytes(rows, E) + align_up(4 * static_cast<size_t>(rows) * K * D) +
+         4 * static_cast<size_t>(rows) * moe::kFewPartCols;
 }
 
 static moe_status run_few(moe::FewProblem& p, void* workspace, size_t workspace_bytes,
@@ -985,10 +986,16 @@ static moe_status run_few(moe::FewProblem& p, void* workspace, size_t workspace_
   }
   if (!is_16bit(p.dtype)) return fail(MOE_ERR_DTYPE, "dtype must be MOE_F16 or MOE_BF16");
   uintptr_t bits = 0;
-  for (const void* q : {p.x, p.wg, p.wu, p.wd, static_cast<const void*>(p.w_router)}) {
+  for (const void* q : {p.x, p.wg, p.wu, p.wd, static_cast<const void*>(p.y),
+                        static_cast<const void*>(p.w_router)}) {
     bits |= reinterpret_cast<uintptr_t>(q);
   }
-  if (bits % 16 != 0) return fail(MOE_ERR_SHAPE, "x, w_router and the weights must be 16-byte aligned");
+  if (p.fmt == moe::kFewMx) {
+    for (const void* q : {p.sg, p.su, p.sd}) bits |= reinterpret_cast<uintptr_t>(q);
+  }
+  if (bits % 16 != 0) {
+    return fail(MOE_ERR_SHAPE, "x, y, w_router, the weights and MXFP4 scales must be 16-byte aligned");
+  }
   const size_t need = moe_few_workspace_bytes(p.T, p.K, p.E, p.D);
   if (workspace_bytes < need) {
     return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
@@ -999,6 +1006,8 @@ static moe_status run_few(moe::FewProblem& p, void* workspace, size_t workspace_
   if (p.T == 0) return ok();
   p.logits = static_cast<float*>(workspace);
   p.hw = static_cast<char*>(workspace) + few_logits_bytes(p.T, p.E);
+  p.parts = reinterpret_cast<float*>(static_cast<char*>(p.hw) +
+                                     align_up(4 * static_cast<size_t>(p.T) * p.K * p.D));
   return hip_status(moe::launch_few(p, stream), what);
 }
 
@@ -1008,7 +1017,7 @@ moe_status moe_layer_few(const void* x, const float* w_router, const float* bias
                          float* topk_weights, void* workspace, size_t workspace_bytes, void* y,
                          void* stream) {
   moe::FewProblem p{x, w_router, bias, w_gate, w_up, w_down, nullptr, nullptr, nullptr, T, H, D, E,
-                    K, renorm, dtype, moe::kFewW16, topk_ids, topk_weights, nullptr, nullptr, y};
+                    K, renorm, dtype, moe::kFewW16, topk_ids, topk_weights, nullptr, nullptr, nullptr, y};
   return run_few(p, workspace, workspace_bytes, static_cast<hipStream_t>(stream), "moe_layer_few launch");
 }
 
@@ -1019,7 +1028,7 @@ moe_status moe_layer_few_w8(const void* x, const float* w_router, const float* b
                             float* topk_weights, void* workspace, size_t workspace_bytes, void* y,
                             void* stream) {
   moe::FewProblem p{x, w_router, bias, w_gate, w_up, w_down, s_gate, s_up, s_down, T, H, D, E, K,
-                    renorm, dtype, moe::kFewFp8, topk_ids, topk_weights, nullptr, nullptr, y};
+                    renorm, dtype, moe::kFewFp8, topk_ids, topk_weights, nullptr, nullptr, nullptr, y};
   return run_few(p, workspace, workspace_bytes, static_cast<hipStream_t>(stream), "moe_layer_few_w8 launch");
 }
 
@@ -1030,7 +1039,7 @@ moe_status moe_layer_few_mx(const void* x, const float* w_router, const float* b
                             int32_t* topk_ids, float* topk_weights, void* workspace,
                             size_t workspace_bytes, void* y, void* stream) {
   moe::FewProblem p{x, w_router, bias, w_gate, w_up, w_down, s_gate, s_up, s_down, T, H, D, E, K,
-                    renorm, dtype, moe::kFewMx, topk_ids, topk_weights, nullptr, nullptr, y};
+                    renorm, dtype, moe::kFewMx, topk_ids, topk_weights, nullptr, nullptr, nullptr, y};
   return run_few(p, workspace, workspace_bytes, static_cast<hipStream_t>(stream), "moe_layer_few_mx launch");
 }
 

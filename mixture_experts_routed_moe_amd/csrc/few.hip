@@ -20,10 +20,10 @@
 //                       and a pass through memory), finds the distinct experts
 //                       and takes (expert, 16 columns) items in turn. Its 4
 //                       waves split the reduction; partial sums meet in LDS.
-//   few_down_kernel     one workgroup per 16 columns of y walks ALL distinct
-//                       experts: row t of the MFMA tile is token t, so one
-//                       accumulator holds y itself and no pass combines expert
-//                       rows. Its waves split the (expert, reduction) stream.
+//   few_down_kernel     a workgroup takes 64 columns of y and a share of the
+//                       distinct experts: row t of the MFMA tile is token t, so
+//                       its accumulators hold parts of y and no pass combines
+//                       expert rows; few_combine_kernel adds up the shares.
 //
 // Both GEMM kernels run one uninterrupted stream of chunks (64 bytes of each
 // of 16 weight rows = 1 KB a load) through a register ring that crosses item
@@ -70,6 +70,7 @@ struct FewArgs {
   int32_t* ids;
   float* weights;
   uint8_t* hw;                    // [P, D] fp32, or two [P, D] bf16 (high, low parts)
+  float* parts;                   // [parts, T, H] sums of few_down_kernel's expert groups
   void* y;
   int T, H, D, E, K, renorm;
 };
@@ -327,20 +328,38 @@ constexpr bool hw_fp32() {
 }
 
 // One step of a wave: a pair of chunks (both halves of the 128-byte lines of 16
-// gate and 16 up rows) and the tokens' x.
-template <int F>
+// NT gate and up rows) and the tokens' x.
+template <int F, int NT>
 struct GateUpSlot {
-  u32x4 g[2], u[2];
+  u32x4 g[NT][2], u[NT][2];
   u32x4 x[2][lane_elems<F>() / 8];
-  uint32_t sg[2], su[2];        // FP8: the rows' fp32 scales (in [0]); MXFP4: E8M0 bytes
+  u32x2 sg[NT], su[NT];         // FP8: the rows' fp32 scales (in .x); MXFP4: the pair's 8 E8M0 bytes
+};
+
+// The E8M0 byte of lane group lg in half k of a pair's 8.
+__device__ __forceinline__ uint32_t pair_scale(const u32x2& s, int k, int lg) {
+  return ((k ? s.y : s.x) >> (8 * lg)) & 0xffu;
+}
+
+// Column tiles of 16 that a wave works on at once, ring depth in pairs and waves
+// per SIMD. x is read once for all tiles: with 4-bit weights its loads would
+// outnumber the weights' two to one at NT = 1 (8 tokens on MXFP4 weights of
+// the 256 x 7168 x 2048 layer: 261 us, 184 us at NT = 2); 16-bit
+// weights are at 5.9 TB/s with one tile and four workgroups on a CU.
+template <int F>
+struct GateUpShape {
+  static constexpr int kTiles = F == kW16 ? 1 : 2;
+  static constexpr int kDepth = F == kW16 ? 4 : 2;
+  static constexpr int kWaves = F == kW16 ? 4 : 2;
 };
 
 template <int DT, int F>
-__global__ __launch_bounds__(kGateUpThreads, 4) void few_gate_up_kernel(FewArgs a) {
-  constexpr int EL = lane_elems<F>(), NX = EL / 8, S = F == kW16 ? 4 : 2;
+__global__ __launch_bounds__(kGateUpThreads, GateUpShape<F>::kWaves) void few_gate_up_kernel(FewArgs a) {
+  constexpr int EL = lane_elems<F>(), NX = EL / 8;
+  constexpr int S = GateUpShape<F>::kDepth, NT = GateUpShape<F>::kTiles;
   __shared__ Plan plan;
   __shared__ float sw[kMaxP];
-  __shared__ f32x4 red[2][4][2][64];
+  __shared__ f32x4 red[2][4][2 * NT][64];
   const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63, lr = lane & 15, lg = lane >> 4;
   const int P = a.T * a.K;
 
@@ -368,7 +387,7 @@ __global__ __launch_bounds__(kGateUpThreads, 4) void few_gate_up_kernel(FewArgs 
     }
   }
 
-  const int tiles = a.D / 16;
+  const int tiles = a.D / (16 * NT);
   const int items = plan.count * tiles;
   if (static_cast<int>(blockIdx.x) >= items) return;
   // This wave's steps of every item: pairs of chunks (128 bytes a row) wave, wave + 4, ...
@@ -382,11 +401,12 @@ __global__ __launch_bounds__(kGateUpThreads, 4) void few_gate_up_kernel(FewArgs 
   int l_item = blockIdx.x, l_c = 0;
   const uint8_t *pg = nullptr, *pu = nullptr, *qg = nullptr, *qu = nullptr;
   const uint32_t w_off = static_cast<uint32_t>(lr * row_bytes) + lg * 16;
-  const uint32_t s_off = F == kWFp8 ? lr * 4 : static_cast<uint32_t>(lr * blocks) + lg;
+  const uint32_t s_off = F == kWFp8 ? lr * 4 : static_cast<uint32_t>(lr * blocks);
+  const int64_t tile_bytes = 16 * row_bytes;
   uint32_t x_off = 0;
   auto aim = [&]() __attribute__((always_inline)) {
     const int e = uniform(plan.list[l_item / tiles]);
-    const int64_t row = static_cast<int64_t>(e) * a.D + (l_item % tiles) * 16;
+    const int64_t row = static_cast<int64_t>(e) * a.D + (l_item % tiles) * (16 * NT);
     pg = a.wg + row * row_bytes;
     pu = a.wu + row * row_bytes;
     if constexpr (F != kW16) {
@@ -397,30 +417,32 @@ __global__ __launch_bounds__(kGateUpThreads, 4) void few_gate_up_kernel(FewArgs 
     x_off = (m >> lr) & 1 ? static_cast<uint32_t>(lr * a.H + lg * EL) * 2 : kNoRow;
   };
   const __amdgpu_buffer_rsrc_t xb = buffer_of(a.x, static_cast<int64_t>(a.T) * a.H * 2);
-  GateUpSlot<F> ring[S];
-  auto load = [&](GateUpSlot<F>& s) __attribute__((always_inline)) {
+  GateUpSlot<F, NT> ring[S];
+  auto load = [&](GateUpSlot<F, NT>& s) __attribute__((always_inline)) {
     // Both halves of a line right after one another: with other loads between
     // them the second one stalls the first-level cache on the pending line.
     const int64_t c = 4 * l_c + wave;
-    const uint8_t *g = pg + c * 128, *u = pu + c * 128;
-    s.g[0] = *reinterpret_cast<const u32x4*>(g + w_off);
-    s.g[1] = *reinterpret_cast<const u32x4*>(g + w_off + 64);
-    s.u[0] = *reinterpret_cast<const u32x4*>(u + w_off);
-    s.u[1] = *reinterpret_cast<const u32x4*>(u + w_off + 64);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const uint8_t *g = pg + t * tile_bytes + c * 128, *u = pu + t * tile_bytes + c * 128;
+      s.g[t][0] = *reinterpret_cast<const u32x4*>(g + w_off);
+      s.g[t][1] = *reinterpret_cast<const u32x4*>(g + w_off + 64);
+      s.u[t][0] = *reinterpret_cast<const u32x4*>(u + w_off);
+      s.u[t][1] = *reinterpret_cast<const u32x4*>(u + w_off + 64);
+      if constexpr (F == kWFp8) {
+        s.sg[t].x = *reinterpret_cast<const uint32_t*>(qg + t * 64 + s_off);
+        s.su[t].x = *reinterpret_cast<const uint32_t*>(qu + t * 64 + s_off);
+      } else if constexpr (F == kWMx) {
+        s.sg[t] = *reinterpret_cast<const u32x2*>(qg + t * 16 * blocks + c * 8 + s_off);
+        s.su[t] = *reinterpret_cast<const u32x2*>(qu + t * 16 * blocks + c * 8 + s_off);
+      }
+    }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
 #pragma unroll
       for (int i = 0; i < NX; ++i) {
         s.x[k][i] = buffer_load16(xb, x_off + 16 * i, static_cast<int>(c) * (16 * EL) + k * (8 * EL));
       }
-      if constexpr (F == kWMx) {
-        s.sg[k] = (qg + c * 8 + k * 4)[s_off];
-        s.su[k] = (qu + c * 8 + k * 4)[s_off];
-      }
-    }
-    if constexpr (F == kWFp8) {
-      s.sg[0] = *reinterpret_cast<const uint32_t*>(qg + s_off);
-      s.su[0] = *reinterpret_cast<const uint32_t*>(qu + s_off);
     }
     if (++l_c == n) {
       // past the last item the last pair is read again (in bounds, never used)
@@ -435,47 +457,55 @@ __global__ __launch_bounds__(kGateUpThreads, 4) void few_gate_up_kernel(FewArgs 
   };
 
   int item = blockIdx.x, buf = 0;
-  f32x4 accg = {}, accu = {};
-  float scale_g = 1.0f, scale_u = 1.0f;
+  f32x4 accg[NT] = {}, accu[NT] = {};
+  float scale_g[NT], scale_u[NT];
   // The item's sums are complete: add up the waves' parts and store hw.
   auto finish = [&]() __attribute__((always_inline)) {
-    red[buf][wave][0][lane] = accg;
-    red[buf][wave][1][lane] = accu;
-    accg = accu = f32x4{};
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      red[buf][wave][2 * t][lane] = accg[t];
+      red[buf][wave][2 * t + 1][lane] = accu[t];
+      accg[t] = accu[t] = f32x4{};
+    }
     wait_lds();
     barrier_no_wait();
-    // thread (wave i, lane l): register i of lane l, row 4 (l / 16) + i
-    float g = 0.0f, u = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      g += reinterpret_cast<const float*>(&red[buf][w][0][lane])[wave];
-      u += reinterpret_cast<const float*>(&red[buf][w][1][lane])[wave];
-    }
     const int e = uniform(plan.list[item / tiles]);
-    const int t = lg * 4 + wave;
-    if ((plan.mask[e] >> t) & 1) {
-      int p = -1;
-      float w = 0.0f;
+    const int t = lg * 4 + wave;     // thread (wave i, lane l): register i of lane l, row 4 (l / 16) + i
+    const bool live = (plan.mask[e] >> t) & 1;
+    int p = 0;
+    float w = 0.0f;
+    if (live) {
       for (int k = a.K - 1; k >= 0; --k) {
         if (plan.sid[t * a.K + k] == e) {
           p = t * a.K + k;
           w += sw[p];
         }
       }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float g = 0.0f, u = 0.0f;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        g += reinterpret_cast<const float*>(&red[buf][v][2 * nt][lane])[wave];
+        u += reinterpret_cast<const float*>(&red[buf][v][2 * nt + 1][lane])[wave];
+      }
       if constexpr (F == kWFp8) {
-        g *= scale_g;
-        u *= scale_u;
+        g *= scale_g[nt];
+        u *= scale_u[nt];
       }
       const float v = w * (silu(g) * u);
-      const int64_t at = static_cast<int64_t>(p) * a.D + (item % tiles) * 16 + lr;
-      if constexpr (hw_fp32<DT, F>()) {
-        reinterpret_cast<float*>(a.hw)[at] = v;
-      } else {
-        uint32_t hi, lo;
-        split_bf16(v, hi, lo);
-        uint16_t* h = reinterpret_cast<uint16_t*>(a.hw);
-        h[at] = static_cast<uint16_t>(hi);
-        h[static_cast<int64_t>(P) * a.D + at] = static_cast<uint16_t>(lo);
+      const int64_t at = static_cast<int64_t>(p) * a.D + (item % tiles) * (16 * NT) + nt * 16 + lr;
+      if (live) {
+        if constexpr (hw_fp32<DT, F>()) {
+          reinterpret_cast<float*>(a.hw)[at] = v;
+        } else {
+          uint32_t hi, lo;
+          split_bf16(v, hi, lo);
+          uint16_t* h = reinterpret_cast<uint16_t*>(a.hw);
+          h[at] = static_cast<uint16_t>(hi);
+          h[static_cast<int64_t>(P) * a.D + at] = static_cast<uint16_t>(lo);
+        }
       }
     }
     buf ^= 1;   // the other buffer: a wave still reading this one has not passed the next barrier
@@ -483,15 +513,16 @@ __global__ __launch_bounds__(kGateUpThreads, 4) void few_gate_up_kernel(FewArgs 
   };
 
   if (n == 0) {                      // fewer pairs than waves: this one only adds zeros
-    if constexpr (F == kWFp8) {
-      while (item < items) {
-        const int64_t row = static_cast<int64_t>(plan.list[item / tiles]) * a.D + (item % tiles) * 16 + lr;
-        scale_g = static_cast<const float*>(a.sg)[row];
-        scale_u = static_cast<const float*>(a.su)[row];
-        finish();
+    while (item < items) {
+      if constexpr (F == kWFp8) {
+        const int64_t row = static_cast<int64_t>(plan.list[item / tiles]) * a.D + (item % tiles) * (16 * NT) + lr;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          scale_g[t] = static_cast<const float*>(a.sg)[row + 16 * t];
+          scale_u[t] = static_cast<const float*>(a.su)[row + 16 * t];
+        }
       }
-    } else {
-      while (item < items) finish();
+      finish();
     }
     return;
   }
@@ -503,27 +534,39 @@ __global__ __launch_bounds__(kGateUpThreads, 4) void few_gate_up_kernel(FewArgs 
     constexpr int s = decltype(U)::value;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      u32x4 wg[NX], wu[NX];
-      decode<DT, F>(ring[s].g[k], ring[s].sg[k], wg);
-      decode<DT, F>(ring[s].u[k], ring[s].su[k], wu);
+      u32x4 xl[F == kWMx && DT == kF16 ? NX : 1];     // fp16 x in two bf16 parts
+      if constexpr (F == kWMx && DT == kF16) {
 #pragma unroll
-      for (int i = 0; i < NX; ++i) {
-        if constexpr (F == kWMx && DT == kF16) {
-          u32x4 hi, lo;
-          split_f16x8(ring[s].x[k][i], hi, lo);
-          accg = mfma16<kBF16>(hi, wg[i], accg);
-          accu = mfma16<kBF16>(hi, wu[i], accu);
-          accg = mfma16<kBF16>(lo, wg[i], accg);
-          accu = mfma16<kBF16>(lo, wu[i], accu);
-        } else {
-          accg = mfma16<DT>(ring[s].x[k][i], wg[i], accg);
-          accu = mfma16<DT>(ring[s].x[k][i], wu[i], accu);
+        for (int i = 0; i < NX; ++i) {
+          const u32x4 x = ring[s].x[k][i];
+          split_f16x8(x, ring[s].x[k][i], xl[i]);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        u32x4 wg[NX], wu[NX];
+        decode<DT, F>(ring[s].g[t][k], pair_scale(ring[s].sg[t], k, lg), wg);
+        decode<DT, F>(ring[s].u[t][k], pair_scale(ring[s].su[t], k, lg), wu);
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+          if constexpr (F == kWMx && DT == kF16) {
+            accg[t] = mfma16<kBF16>(ring[s].x[k][i], wg[i], accg[t]);
+            accu[t] = mfma16<kBF16>(ring[s].x[k][i], wu[i], accu[t]);
+            accg[t] = mfma16<kBF16>(xl[i], wg[i], accg[t]);
+            accu[t] = mfma16<kBF16>(xl[i], wu[i], accu[t]);
+          } else {
+            accg[t] = mfma16<DT>(ring[s].x[k][i], wg[i], accg[t]);
+            accu[t] = mfma16<DT>(ring[s].x[k][i], wu[i], accu[t]);
+          }
         }
       }
     }
     if constexpr (F == kWFp8) {
-      scale_g = __uint_as_float(ring[s].sg[0]);
-      scale_u = __uint_as_float(ring[s].su[0]);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        scale_g[t] = __uint_as_float(ring[s].sg[t].x);
+        scale_u[t] = __uint_as_float(ring[s].su[t].x);
+      }
     }
     load(ring[s]);
     if (++c == n) {
@@ -543,19 +586,30 @@ __global__ __launch_bounds__(kGateUpThreads, 4) void few_gate_up_kernel(FewArgs 
 
 // ------------------------------------------------------------------- down --
 
-template <int DT, int F>
+// Column tiles of 16 that a wave works on at once, waves of a workgroup and
+// ring depth in pairs. The hidden values of a chunk take 2 (16-bit weights), 4
+// (FP8) or 8 (MXFP4) loads against one of the weights, so they are read once
+// for four tiles; the experts are then split over workgroups instead of the
+// columns, and a last kernel adds up the parts.
+constexpr int kDownTiles = 4;
+constexpr int kDownWaves = 4;
+constexpr int kDownFill = 512;            // workgroups that run at once: two on a CU
+template <int F>
+constexpr int kDownDepth = F == kW16 ? 3 : (F == kWFp8 ? 2 : 1);
+
+template <int F>
 struct DownSlot {
-  u32x4 w[2];
+  u32x4 w[kDownTiles][2];
   u32x4 h[2][lane_elems<F>() / 4];   // hw: fp32 (8 elements in 2), or the high parts, then the low parts
-  uint32_t s[2];
+  u32x2 s[kDownTiles];
 };
 
-template <int DT, int F, int NW>
-__global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs a) {
-  constexpr int EL = lane_elems<F>(), NX = EL / 8, S = F == kW16 ? 4 : (F == kWFp8 ? 2 : 1);
+template <int DT, int F>
+__global__ __launch_bounds__(64 * kDownWaves, 2) void few_down_kernel(FewArgs a) {
+  constexpr int EL = lane_elems<F>(), NX = EL / 8, S = kDownDepth<F>, NT = kDownTiles, NW = kDownWaves;
   __shared__ Plan plan;
   __shared__ uint16_t pair[kMaxE * kRows];   // hw row of (distinct expert, token)
-  __shared__ f32x4 red[NW][64];
+  __shared__ f32x4 red[NW][NT][64];
   const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63, lr = lane & 15, lg = lane >> 4;
   const int P = a.T * a.K;
   for (int p = tid; p < P; p += 64 * NW) {
@@ -577,35 +631,43 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs a) {
   }
   __syncthreads();
 
-  const int col = blockIdx.x * 16 + lr;
+  const int col0 = blockIdx.x * (16 * NT);
   const int pairs = a.D / (8 * EL);                 // 128-byte pieces of a weight row
   const int64_t row_bytes = static_cast<int64_t>(a.D / EL) * 16;
-  const int total = plan.count * pairs;
-  const int u0 = static_cast<int>(static_cast<int64_t>(total) * wave / NW);
-  const int u1 = static_cast<int>(static_cast<int64_t>(total) * (wave + 1) / NW);
+  const int64_t blocks = a.D / 32;
+  // This wave's share of the (expert, piece) stream.
+  const int64_t total = static_cast<int64_t>(plan.count) * pairs;
+  const int parts = gridDim.y * NW, part = blockIdx.y * NW + wave;
+  const int u0 = static_cast<int>(total * part / parts);
+  const int u1 = static_cast<int>(total * (part + 1) / parts);
 
-  f32x4 sum = {}, acc = {};
+  f32x4 sum[NT] = {}, acc[NT] = {};
   if (u0 < u1) {
     int l_j = u0 / pairs, l_c = u0 % pairs, l_left = u1 - u0;
     const uint8_t *pw = nullptr, *q = nullptr;
     const uint32_t w_off = static_cast<uint32_t>(lr * row_bytes) + lg * 16;
-    const uint32_t s_off = F == kWFp8 ? lr * 4 : static_cast<uint32_t>(lr * (a.D / 32)) + lg;
+    const uint32_t s_off = F == kWFp8 ? lr * 4 : static_cast<uint32_t>(lr * blocks);
     const int64_t half = static_cast<int64_t>(P) * a.D * 2;
     const __amdgpu_buffer_rsrc_t hb = buffer_of(a.hw, hw_fp32<DT, F>() ? 2 * half : half);
     const __amdgpu_buffer_rsrc_t lb = buffer_of(a.hw + half, half);
     uint32_t h_off = 0;
     auto aim = [&]() __attribute__((always_inline)) {
-      const int64_t row = static_cast<int64_t>(uniform(plan.list[l_j])) * a.H + blockIdx.x * 16;
+      const int64_t row = static_cast<int64_t>(uniform(plan.list[l_j])) * a.H + col0;
       pw = a.wd + row * row_bytes;
-      if constexpr (F != kW16) q = static_cast<const uint8_t*>(a.sd) + row * (F == kWFp8 ? 4 : a.D / 32);
+      if constexpr (F != kW16) q = static_cast<const uint8_t*>(a.sd) + row * (F == kWFp8 ? 4 : blocks);
       const int p = pair[l_j * kRows + lr];
       h_off = p < kMaxP ? static_cast<uint32_t>(p * a.D + lg * EL) * (hw_fp32<DT, F>() ? 4 : 2) : kNoRow;
     };
-    DownSlot<DT, F> ring[S];
-    auto load = [&](DownSlot<DT, F>& s) __attribute__((always_inline)) {
-      const uint8_t* w = pw + static_cast<int64_t>(l_c) * 128;
-      s.w[0] = *reinterpret_cast<const u32x4*>(w + w_off);
-      s.w[1] = *reinterpret_cast<const u32x4*>(w + w_off + 64);
+    DownSlot<F> ring[S];
+    auto load = [&](DownSlot<F>& s) __attribute__((always_inline)) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const uint8_t* w = pw + t * (16 * row_bytes) + static_cast<int64_t>(l_c) * 128;
+        s.w[t][0] = *reinterpret_cast<const u32x4*>(w + w_off);
+        s.w[t][1] = *reinterpret_cast<const u32x4*>(w + w_off + 64);
+        if constexpr (F == kWFp8) s.s[t].x = *reinterpret_cast<const uint32_t*>(q + t * 64 + s_off);
+        else if constexpr (F == kWMx) s.s[t] = *reinterpret_cast<const u32x2*>(q + t * 16 * blocks + l_c * 8 + s_off);
+      }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         if constexpr (hw_fp32<DT, F>()) {
@@ -618,9 +680,7 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs a) {
             s.h[k][NX + i] = buffer_load16(lb, h_off + 16 * i, (2 * l_c + k) * (8 * EL));
           }
         }
-        if constexpr (F == kWMx) s.s[k] = (q + l_c * 8 + k * 4)[s_off];
       }
-      if constexpr (F == kWFp8) s.s[0] = *reinterpret_cast<const uint32_t*>(q + s_off);
       if (--l_left > 0) {
         if (++l_c == pairs) {
           l_c = 0;
@@ -636,25 +696,31 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs a) {
     auto step = [&](auto U) __attribute__((always_inline)) {
       constexpr int s = decltype(U)::value;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if constexpr (hw_fp32<DT, F>()) {
+      for (int t = 0; t < NT; ++t) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t w = ring[s].w[k][i >> 1];
-            acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(ring[s].h[k][i >> 2][i & 3]),
-                                                       f16_to_float((i & 1) ? (w >> 16) : (w & 0xffffu)), acc, 0, 0, 0);
-          }
-        } else {
-          u32x4 w[NX];
-          decode<kBF16, F>(ring[s].w[k], ring[s].s[k], w);
+        for (int k = 0; k < 2; ++k) {
+          if constexpr (hw_fp32<DT, F>()) {
 #pragma unroll
-          for (int i = 0; i < NX; ++i) {
-            acc = mfma16<kBF16>(ring[s].h[k][i], w[i], acc);
-            acc = mfma16<kBF16>(ring[s].h[k][NX + i], w[i], acc);
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t w = ring[s].w[t][k][i >> 1];
+              acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(ring[s].h[k][i >> 2][i & 3]),
+                                                            f16_to_float((i & 1) ? (w >> 16) : (w & 0xffffu)), acc[t],
+                                                            0, 0, 0);
+            }
+          } else {
+            u32x4 w[NX];
+            decode<kBF16, F>(ring[s].w[t][k], pair_scale(ring[s].s[t], k, lg), w);
+#pragma unroll
+            for (int i = 0; i < NX; ++i) {
+              acc[t] = mfma16<kBF16>(ring[s].h[k][i], w[i], acc[t]);
+              acc[t] = mfma16<kBF16>(ring[s].h[k][NX + i], w[i], acc[t]);
+            }
           }
         }
       }
-      const float scale = F == kWFp8 ? __uint_as_float(ring[s].s[0]) : 1.0f;
+      float scale[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) scale[t] = F == kWFp8 ? __uint_as_float(ring[s].s[t].x) : 1.0f;
       load(ring[s]);
       --left;
       if (++c == pairs || left == 0) {      // this wave's part of expert j is complete
@@ -662,8 +728,11 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs a) {
         const uint32_t m = static_cast<uint32_t>(uniform(plan.mask[plan.list[j]])) >> (lg * 4);
         ++j;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum[i] += (m >> i) & 1 ? acc[i] * scale : 0.0f;
-        acc = f32x4{};
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum[t][i] += (m >> i) & 1 ? acc[t][i] * scale[t] : 0.0f;
+          acc[t] = f32x4{};
+        }
       }
     };
     const int mine = left;
@@ -672,16 +741,37 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs a) {
       if (decltype(U)::value < mine % S) step(U);
     });
   }
-  red[wave][lane] = sum;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) red[wave][t][lane] = sum[t];
   __syncthreads();
-  if (tid < 256) {                       // register tid / 64 of lane tid % 64
-    const int t = lg * 4 + wave;
-    float v = 0.0f;
-    for (int w = 0; w < NW; ++w) v += reinterpret_cast<const float*>(&red[w][lane])[wave];
-    if (t < a.T) {
-      static_cast<uint16_t*>(a.y)[static_cast<int64_t>(t) * a.H + col] = static_cast<uint16_t>(from_float<DT>(v));
+  const int t = lg * 4 + wave;             // register `wave` of lane `lane`
+  if (t < a.T) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) v += reinterpret_cast<const float*>(&red[w][nt][lane])[wave];
+      const int64_t at = static_cast<int64_t>(t) * a.H + col0 + nt * 16 + lr;
+      if (gridDim.y == 1) {
+        static_cast<uint16_t*>(a.y)[at] = static_cast<uint16_t>(from_float<DT>(v));
+      } else {
+        a.parts[static_cast<int64_t>(blockIdx.y) * a.T * a.H + at] = v;
+      }
     }
   }
+}
+
+// y = R(the sum of `count` parts [T, H], in order), four values a thread.
+template <int DT>
+__global__ __launch_bounds__(256) void few_combine_kernel(const float* __restrict__ parts, int count,
+                                                          int64_t n, uint16_t* __restrict__ y) {
+  const int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (at >= n) return;
+  f32x4 v = {};
+#pragma unroll 4
+  for (int g = 0; g < count; ++g) v += *reinterpret_cast<const f32x4*>(parts + g * n + at);
+  *reinterpret_cast<u32x2*>(y + at) = u32x2{from_float<DT>(v[0]) | (from_float<DT>(v[1]) << 16),
+                                           from_float<DT>(v[2]) | (from_float<DT>(v[3]) << 16)};
 }
 
 // ----------------------------------------------------------------- launch --
@@ -703,26 +793,33 @@ template <int DT, int F>
 hipError_t launch_typed(const FewProblem& p, hipStream_t st) {
   FewArgs a{p.x, static_cast<const uint8_t*>(p.wg), static_cast<const uint8_t*>(p.wu),
             static_cast<const uint8_t*>(p.wd), p.sg, p.su, p.sd, nullptr, p.ids, p.weights,
-            static_cast<uint8_t*>(p.hw), p.y, p.T, p.H, p.D, p.E, p.K, p.renorm};
+            static_cast<uint8_t*>(p.hw), p.parts, p.y, p.T, p.H, p.D, p.E, p.K, p.renorm};
   if (p.w_router) {
     launch_logits<DT>(p, st);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
     a.logits = p.logits;
   }
-  // Items of the most experts there can be; four workgroups fit a CU.
+  // Items of the most experts there can be.
   const int most = p.T * p.K < p.E ? p.T * p.K : p.E;
-  const int64_t items = static_cast<int64_t>(most) * (p.D / 16);
-  const int grid = static_cast<int>(items < 1024 ? items : 1024);
+  const int64_t items = static_cast<int64_t>(most) * (p.D / (16 * GateUpShape<F>::kTiles));
+  constexpr int kFill = 256 * GateUpShape<F>::kWaves;     // workgroups that run at once
+  const int grid = static_cast<int>(items < kFill ? items : kFill);
   hipLaunchKernelGGL((few_gate_up_kernel<DT, F>), dim3(grid), dim3(kGateUpThreads), 0, st, a);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  const int cols = p.H / 16;
-  if (cols <= 256) {
-    hipLaunchKernelGGL((few_down_kernel<DT, F, 16>), dim3(cols), dim3(1024), 0, st, a);
-  } else {
-    hipLaunchKernelGGL((few_down_kernel<DT, F, 8>), dim3(cols), dim3(512), 0, st, a);
-  }
+  const int tiles = p.H / (16 * kDownTiles);
+  const int64_t pieces = static_cast<int64_t>(most) * (p.D / (8 * lane_elems<F>()));
+  int parts = kDownFill / tiles;
+  // at least two pieces a wave; one part writes y itself
+  if (parts > pieces / (2 * kDownWaves)) parts = static_cast<int>(pieces / (2 * kDownWaves));
+  if (parts < 1) parts = 1;
+  hipLaunchKernelGGL((few_down_kernel<DT, F>), dim3(tiles, parts), dim3(64 * kDownWaves), 0, st, a);
+  err = hipGetLastError();
+  if (err != hipSuccess || parts == 1) return err;
+  const int64_t n = static_cast<int64_t>(p.T) * p.H;
+  hipLaunchKernelGGL(few_combine_kernel<DT>, dim3(static_cast<unsigned>((n + 1023) / 1024)), dim3(256), 0,
+                     st, p.parts, parts, n, static_cast<uint16_t*>(p.y));
   return hipGetLastError();
 }
 

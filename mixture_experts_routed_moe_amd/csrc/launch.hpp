@@ -134,6 +134,7 @@ hipError_t launch_block_norm(const NormProblem& p, hipStream_t stream);
 
 // A whole layer for at most 16 tokens (few.hip).
 constexpr int kFewW16 = 0, kFewFp8 = 1, kFewMx = 2;
+constexpr int kFewPartCols = 512 * 64;   // parts x columns of the down kernel at most
 struct FewProblem {
   const void* x;            // [T, H] of dtype (kF16 / kBF16)
   const float* w_router;    // [E, H], or nullptr: ids and weights are given
@@ -145,6 +146,7 @@ struct FewProblem {
   float* weights;           // [T, K]; nullptr (given routing) = ones
   float* logits;            // workspace [T, E]
   void* hw;                 // workspace [T * K, D], 4 bytes each
+  float* parts;             // workspace, kFewPartCols floats a token
   void* y;
 };
 hipError_t launch_few(const FewProblem& p, hipStream_t stream);

@@ -25,7 +25,7 @@ def _few(fmt="", x=A, router=A, bias=None, w=A, s=A, T=4, H=256, D=256, E=8, K=2
     (dict(H=1 << 25), SHAPE), (dict(D=0), SHAPE), (dict(D=192), SHAPE), (dict(E=0), SHAPE), (dict(E=1025), SHAPE),
     (dict(K=0), SHAPE), (dict(K=65, E=100), SHAPE), (dict(K=9), SHAPE), (dict(T=16, K=64, E=64, D=1 << 20), SHAPE),
     (dict(dtype=2), DTYPE), (dict(dtype=7), DTYPE),
-    (dict(x=A + 2), SHAPE), (dict(w=A + 8), SHAPE), (dict(router=A + 4), SHAPE),
+    (dict(x=A + 2), SHAPE), (dict(w=A + 8), SHAPE), (dict(router=A + 4), SHAPE), (dict(y=A + 2), SHAPE),
     (dict(ws_bytes=0), WORKSPACE), (dict(ws=A + 16), WORKSPACE),
 ])
 def test_refusals(fmt, bad, status):
@@ -35,12 +35,12 @@ def test_refusals(fmt, bad, status):
 
 def test_scales_and_block_rows():
     assert _few("_w8", s=None) == NULL and _few("_mx", s=None) == NULL
-    assert _few("_mx", D=128) == SHAPE
+    assert _few("_mx", D=128) == SHAPE and _few("_mx", s=A + 8) == SHAPE
 
 
 def test_workspace_bytes():
     f = _lib.lib().moe_few_workspace_bytes
-    assert f(16, 8, 256, 2048) == 16 * 256 * 4 + 16 * 8 * 2048 * 4
+    assert f(16, 8, 256, 2048) == 16 * 256 * 4 + 16 * 8 * 2048 * 4 + 16 * 32768 * 4   # logits, hidden, parts of y
     assert f(17, 8, 256, 2048) == 0 and f(1, 8, 256, 100) == 0 and f(1, 0, 256, 128) == 0
     n = f(4, 2, 8, 256)
     assert _few(ws_bytes=n - 1) == WORKSPACE
