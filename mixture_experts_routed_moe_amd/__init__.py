@@ -12,7 +12,6 @@ MoeError with the library's status code on any failure.
     y = moe_reduce_fused(expert_out, token_topk_to_pos, topk_weights)  # step 3 alone
     residual, h = moe_block_norm(y, residual, gamma_post, gamma_pre)   # the norms between blocks
 """
-import contextlib
 import ctypes
 import math
 
@@ -950,12 +949,15 @@ def moe_reduce_fused(expert_out, token_topk_to_pos, topk_weights=None, out_dtype
     return y
 
 
-_NO_GUARD = contextlib.nullcontext()
-
-
-def _on(device):
-    """The device of the operands as the current one (a launch goes to the current device)."""
-    return _NO_GUARD if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+def _launch(device, fn, *args):
+    """check(fn(*args)) with `device` as the current one, to which a launch goes."""
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args)
+    if status:
+        check(status)
 
 
 _GATE_NONE, _GATE_CHANNEL, _GATE_TOKEN, _GATE_FULL = 0, 1, 2, 3
@@ -985,7 +987,7 @@ def _output(t, name, shape, dtype, device):
     """An output tensor: the caller's, checked, or a new one."""
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    _check_tensor(t, name, dtype, len(shape), device)
+    _check_tensor(t, name, dtype, None, device)
     if t.shape != shape:
         raise MoeError(MOE_ERR_SHAPE, "%s must be %s (got %s)" % (name, shape, tuple(t.shape)))
     return t
@@ -1007,12 +1009,15 @@ def _run_norm(fn, head, dtype, T, H, residual, gamma_post, gamma_pre, gate, alph
             if g.shape[0] != H:
                 raise MoeError(MOE_ERR_SHAPE, "%s must be [%d]" % (n, H))
     kind = _norm_gate(gate, T, H, dtype, dev)
+    shape = residual.shape
     if has_y:
-        residual_out = _output(residual_out, "residual_out", (T, H), residual.dtype, dev)
+        residual_out = (torch.empty_like(residual) if residual_out is None
+                        else _output(residual_out, "residual_out", shape, residual.dtype, dev))
     elif residual_out is not None:
         raise MoeError(MOE_ERR_NULL, "without y there is no residual_out")
     if gamma_pre is not None:
-        h = _output(h, "h", (T, H), dtype, dev)
+        h = (torch.empty_like(residual) if h is None and dtype == residual.dtype
+             else _output(h, "h", shape, dtype, dev))
     elif h is not None or quant is not None:
         raise MoeError(MOE_ERR_NULL, "h and codes need gamma_pre")
     qcode = 0
@@ -1029,10 +1034,9 @@ def _run_norm(fn, head, dtype, T, H, residual, gamma_post, gamma_pre, gate, alph
     elif codes is not None or scales is not None:
         raise MoeError(MOE_ERR_NULL, "codes and scales need a quant")
     if T:
-        with _on(dev):
-            check(fn(*head, _ptr(residual), _ptr(gamma_post), _ptr(gate), kind, alpha,
-                     _ptr(gamma_pre), eps, T, H, code, _DTYPE_CODE[residual.dtype],
-                     _ptr(residual_out), _ptr(h), qcode, _ptr(codes), _ptr(scales), _stream(dev)))
+        _launch(dev, fn, *head, _ptr(residual), _ptr(gamma_post), _ptr(gate), kind, alpha,
+                _ptr(gamma_pre), eps, T, H, code, _DTYPE_CODE[residual.dtype], _ptr(residual_out),
+                _ptr(h), qcode, _ptr(codes), _ptr(scales), _stream(dev))
     return (residual_out, h) if quant is None else (residual_out, h, codes, scales)
 
 
@@ -1139,10 +1143,9 @@ def _few(x, w_router, bias, w_gate, w_up, w_down, K, renorm, ids, weights, works
         else:
             fn = lib().moe_layer_few
             w = (_ptr(w_gate), _ptr(w_up), _ptr(w_down))
-        with _on(dev):
-            check(fn(_ptr(x), _ptr(w_router), _ptr(bias), *w, T, H, D, E, K, int(bool(renorm)),
-                     _DTYPE_CODE[x.dtype], _ptr(ids), _ptr(weights), _ptr(workspace),
-                     workspace.numel(), _ptr(y), _stream(dev)))
+        _launch(dev, fn, _ptr(x), _ptr(w_router), _ptr(bias), *w, T, H, D, E, K, int(bool(renorm)),
+                _DTYPE_CODE[x.dtype], _ptr(ids), _ptr(weights), _ptr(workspace), workspace.numel(),
+                _ptr(y), _stream(dev))
     return y
 
 
@@ -1223,10 +1226,9 @@ def moe_expert_gate_up_mx4(xq, xs, w_gate, w_up, tables, hq=None, hs=None):
     P = tables.T * tables.K
     hq = _output(hq, "hq", (P, D // 2), torch.uint8, dev)
     hs = _output(hs, "hs", (P, D // 32), torch.uint8, dev)
-    with _on(dev):
-        check(lib().moe_expert_gate_up_mx4(_ptr(xq), _ptr(xs), _ptr(w_gate.packed), _ptr(w_up.packed),
-                                           _ptr(w_gate.scales), _ptr(w_up.scales), tables.ref, H, D,
-                                           _ptr(hq), _ptr(hs), _stream(dev)))
+    _launch(dev, lib().moe_expert_gate_up_mx4, _ptr(xq), _ptr(xs), _ptr(w_gate.packed),
+            _ptr(w_up.packed), _ptr(w_gate.scales), _ptr(w_up.scales), tables.ref, H, D, _ptr(hq),
+            _ptr(hs), _stream(dev))
     return hq, hs
 
 
@@ -1243,10 +1245,8 @@ def moe_expert_down_mx4(hq, hs, w_down, tables, dtype=torch.bfloat16, expert_out
     if tuple(w_down.shape) != (tables.E, H, D):
         raise MoeError(MOE_ERR_SHAPE, "w_down must be [%d, H, %d] (got %s)" % (tables.E, D, tuple(w_down.shape)))
     expert_out = _output(expert_out, "expert_out", (P, H), dtype, dev)
-    with _on(dev):
-        check(lib().moe_expert_down_mx4(_ptr(hq), _ptr(hs), _ptr(w_down.packed), _ptr(w_down.scales),
-                                        tables.ref, H, D, _DTYPE_CODE[dtype], _ptr(expert_out),
-                                        _stream(dev)))
+    _launch(dev, lib().moe_expert_down_mx4, _ptr(hq), _ptr(hs), _ptr(w_down.packed),
+            _ptr(w_down.scales), tables.ref, H, D, _DTYPE_CODE[dtype], _ptr(expert_out), _stream(dev))
     return expert_out
 
 
@@ -1284,9 +1284,8 @@ def moe_routed_forward_mx4(x, w_gate, w_up, w_down, tables, y=None, workspace=No
         workspace = forward_mx4_workspace(tables, H, D, x.dtype)[0]
     _check_tensor(workspace, "workspace", torch.uint8, 1, dev)
     y = _output(y, "y", (T, H), x.dtype, dev)
-    with _on(dev):
-        check(lib().moe_routed_forward_mx4(_ptr(x), _ptr(w_gate.packed), _ptr(w_up.packed),
-                                           _ptr(w_down.packed), _ptr(w_gate.scales), _ptr(w_up.scales),
-                                           _ptr(w_down.scales), tables.ref, H, D, _DTYPE_CODE[x.dtype],
-                                           _ptr(workspace), workspace.numel(), _ptr(y), _stream(dev)))
+    _launch(dev, lib().moe_routed_forward_mx4, _ptr(x), _ptr(w_gate.packed), _ptr(w_up.packed),
+            _ptr(w_down.packed), _ptr(w_gate.scales), _ptr(w_up.scales), _ptr(w_down.scales),
+            tables.ref, H, D, _DTYPE_CODE[x.dtype], _ptr(workspace), workspace.numel(), _ptr(y),
+            _stream(dev))
     return y

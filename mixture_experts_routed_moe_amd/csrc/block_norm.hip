@@ -278,8 +278,13 @@ hipError_t launch_nv(const NormProblem& a, hipStream_t stream) {
 template <int DT, int RDT>
 hipError_t launch_typed(const NormProblem& a, hipStream_t stream) {
   if (!a.vec) return launch_nv<DT, RDT, 1, 16>(a, stream);     // up to 16384 values
-  if (a.H <= 8 * kMaxThreads) return launch_nv<DT, RDT, 8, 1>(a, stream);
-  return launch_nv<DT, RDT, 8, 2>(a, stream);
+  // Two vectors a thread where rows are long and there are more of them than
+  // CUs: more, smaller workgroups then overlap their reductions' waits. H =
+  // 7168: T = 4096 58.8 -> 53.4 us (4.4 TB/s), the combine of 512 x 8 rows 19.1
+  // -> 16.4; but one token 3.8 -> 4.4, and T = 777 of H = 2048 9.2 -> 10.1.
+  // (Four vectors: 57.3, 22.8, 5.6, 12.1.)
+  const bool two = a.H > 8 * kMaxThreads || (a.H > 4 * kMaxThreads && a.T >= 256);
+  return two ? launch_nv<DT, RDT, 8, 2>(a, stream) : launch_nv<DT, RDT, 8, 1>(a, stream);
 }
 
 }  // namespace
