@@ -149,14 +149,31 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
 }
 
+// The wave's sum, in every lane, the same way (lanes without a source add 0).
+__device__ __forceinline__ float wave_sum(float v) {
+#define MOE_DPP_ADD(ctrl, rows)                                                                      \
+  v += __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_update_dpp(                            \
+      0, static_cast<int>(__float_as_uint(v)), ctrl, rows, 0xf, false)))
+  MOE_DPP_ADD(0x111, 0xf);
+  MOE_DPP_ADD(0x112, 0xf);
+  MOE_DPP_ADD(0x114, 0xf);
+  MOE_DPP_ADD(0x118, 0xf);
+  MOE_DPP_ADD(0x142, 0xa);
+  MOE_DPP_ADD(0x143, 0xc);
+#undef MOE_DPP_ADD
+  return __uint_as_float(static_cast<uint32_t>(
+      __builtin_amdgcn_readlane(static_cast<int>(__float_as_uint(v)), 63)));
+}
+
 // Top-k of one token by one wave: lane L holds experts L * NPL .. + NPL - 1,
-// so the lowest lane with the maximum holds the lowest expert index.
+// so the lowest lane with the maximum holds the lowest expert index. (Several
+// tokens side by side in one wave measured slower: the larger code has to be
+// fetched by every CU before its first weight load.)
 template <int NPL>
-__device__ void select_topk(const float* logits, int E, int K, int renorm, int lane, int* sid,
-                            float* sw) {
-  uint32_t key[NPL];
-  uint32_t best = 0u;
-  int best_j = 0;
+__device__ __forceinline__ void select_topk(const float* logits, int E, int K, int renorm, int lane,
+                                            int* sid, float* sw) {
+  uint32_t key[NPL], best;
+  int best_j;
 #pragma unroll
   for (int j = 0; j < NPL; ++j) {
     const int e = lane * NPL + j;
@@ -167,46 +184,31 @@ __device__ void select_topk(const float* logits, int E, int K, int renorm, int l
     best_j = 0;
 #pragma unroll
     for (int j = 1; j < NPL; ++j) {
-      if (key[j] > best) {
-        best = key[j];
-        best_j = j;
-      }
+      const bool more = key[j] > best;
+      best = more ? key[j] : best;
+      best_j = more ? j : best_j;
     }
   };
   rescan();
   const float top = key_value(wave_max(best));
   float z = 0.0f;
 #pragma unroll
-  for (int j = 0; j < NPL; ++j) {
-    if (key[j]) z += expf(key_value(key[j]) - top);
-  }
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) z += __shfl_xor(z, off);
+  for (int j = 0; j < NPL; ++j) z += key[j] ? expf(key_value(key[j]) - top) : 0.0f;
+  z = wave_sum(z);
   float mine = 0.0f;            // lane k keeps the k-th selection (K <= 64)
   int mine_id = 0;
   for (int k = 0; k < K; ++k) {
     const uint32_t m = wave_max(best);
     const int src = __builtin_ctzll(__ballot(best == m));
     const int id = __builtin_amdgcn_readlane(lane * NPL + best_j, src);
-    if (lane == k) {
-      mine = key_value(m);
-      mine_id = id;
-    }
-    if (lane == src) {
+    mine = lane == k ? key_value(m) : mine;
+    mine_id = lane == k ? id : mine_id;
 #pragma unroll
-      for (int j = 0; j < NPL; ++j) {
-        if (j == best_j) key[j] = 0u;
-      }
-      rescan();
-    }
+    for (int j = 0; j < NPL; ++j) key[j] = lane * NPL + j == id ? 0u : key[j];
+    rescan();
   }
   float p = lane < K ? expf(mine - top) / z : 0.0f;
-  if (renorm) {
-    float s = p;
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off);
-    p = p / s;
-  }
+  if (renorm) p = p / wave_sum(p);
   if (lane < K) {
     sid[lane] = mine_id;
     sw[lane] = p;
@@ -343,13 +345,15 @@ __device__ __forceinline__ uint32_t pair_scale(const u32x2& s, int k, int lg) {
 
 // Column tiles of 16 that a wave works on at once, ring depth in pairs and waves
 // per SIMD. x is read once for all tiles: with 4-bit weights its loads would
-// outnumber the weights' two to one at NT = 1 (8 tokens on MXFP4 weights of
-// the 256 x 7168 x 2048 layer: 261 us, 184 us at NT = 2); 16-bit
-// weights are at 5.9 TB/s with one tile and four workgroups on a CU.
+// outnumber the weights' two to one at one tile (8 tokens on MXFP4 weights of
+// the 256 x 7168 x 2048 layer: 261 us, 184 us with two, 202 us with four). 16-bit
+// weights stream at 5.9 TB/s with one tile and four workgroups on a CU (16 tokens
+// 1008 us for 5.98 GB). Rings of 2, 3 and 4 pairs: one token 83.0, 81.7, 84.5 us,
+// on the 128 x 2048 x 768 layer 17.0, 16.5, 18.7 us.
 template <int F>
 struct GateUpShape {
   static constexpr int kTiles = F == kW16 ? 1 : 2;
-  static constexpr int kDepth = F == kW16 ? 4 : 2;
+  static constexpr int kDepth = F == kW16 ? 3 : 2;
   static constexpr int kWaves = F == kW16 ? 4 : 2;
 };
 
@@ -366,11 +370,8 @@ __global__ __launch_bounds__(kGateUpThreads, GateUpShape<F>::kWaves) void few_ga
   if (a.logits) {
     for (int t = wave; t < a.T; t += 4) {
       const float* l = a.logits + static_cast<int64_t>(t) * a.E;
-      int* sid = plan.sid + t * a.K;
-      float* w = sw + t * a.K;
-      if (a.E <= 64) select_topk<1>(l, a.E, a.K, a.renorm, lane, sid, w);
-      else if (a.E <= 256) select_topk<4>(l, a.E, a.K, a.renorm, lane, sid, w);
-      else select_topk<16>(l, a.E, a.K, a.renorm, lane, sid, w);
+      if (a.E > 256) select_topk<16>(l, a.E, a.K, a.renorm, lane, plan.sid + t * a.K, sw + t * a.K);
+      else select_topk<4>(l, a.E, a.K, a.renorm, lane, plan.sid + t * a.K, sw + t * a.K);
     }
   } else {
     for (int p = tid; p < P; p += kGateUpThreads) {
@@ -589,9 +590,15 @@ __global__ __launch_bounds__(kGateUpThreads, GateUpShape<F>::kWaves) void few_ga
 // Column tiles of 16 that a wave works on at once, waves of a workgroup and
 // ring depth in pairs. The hidden values of a chunk take 2 (16-bit weights), 4
 // (FP8) or 8 (MXFP4) loads against one of the weights, so they are read once
-// for four tiles; the experts are then split over workgroups instead of the
-// columns, and a last kernel adds up the parts.
-constexpr int kDownTiles = 4;
+// for four (eight) tiles; the experts are then split over workgroups instead of
+// the columns, and a last kernel adds up the parts. 256 x 7168 x 2048 layer
+// against one tile a wave: 16 tokens 610 -> 509 us (5.9 TB/s), one token 56 ->
+// 47 us, 8 tokens on MXFP4 223 -> 103 us (four tiles: 116). The last kernel
+// takes 4 to 5 us, most of it its launch; adding up in this one by the last
+// workgroup of each column tile needs a fence over the XCDs in every workgroup
+// and took 59 us against 10.6 + 3.9 on the 128 x 2048 x 768 layer.
+template <int F>
+constexpr int kDownTiles = F == kWMx ? 8 : 4;
 constexpr int kDownWaves = 4;
 constexpr int kDownFill = 512;            // workgroups that run at once: two on a CU
 template <int F>
@@ -599,14 +606,14 @@ constexpr int kDownDepth = F == kW16 ? 3 : (F == kWFp8 ? 2 : 1);
 
 template <int F>
 struct DownSlot {
-  u32x4 w[kDownTiles][2];
+  u32x4 w[kDownTiles<F>][2];
   u32x4 h[2][lane_elems<F>() / 4];   // hw: fp32 (8 elements in 2), or the high parts, then the low parts
-  u32x2 s[kDownTiles];
+  u32x2 s[kDownTiles<F>];
 };
 
 template <int DT, int F>
 __global__ __launch_bounds__(64 * kDownWaves, 2) void few_down_kernel(FewArgs a) {
-  constexpr int EL = lane_elems<F>(), NX = EL / 8, S = kDownDepth<F>, NT = kDownTiles, NW = kDownWaves;
+  constexpr int EL = lane_elems<F>(), NX = EL / 8, S = kDownDepth<F>, NT = kDownTiles<F>, NW = kDownWaves;
   __shared__ Plan plan;
   __shared__ uint16_t pair[kMaxE * kRows];   // hw row of (distinct expert, token)
   __shared__ f32x4 red[NW][NT][64];
@@ -808,7 +815,7 @@ hipError_t launch_typed(const FewProblem& p, hipStream_t st) {
   hipLaunchKernelGGL((few_gate_up_kernel<DT, F>), dim3(grid), dim3(kGateUpThreads), 0, st, a);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  const int tiles = p.H / (16 * kDownTiles);
+  const int tiles = p.H / (16 * kDownTiles<F>);
   const int64_t pieces = static_cast<int64_t>(most) * (p.D / (8 * lane_elems<F>()));
   int parts = kDownFill / tiles;
   // at least two pieces a wave; one part writes y itself

@@ -134,7 +134,7 @@ hipError_t launch_block_norm(const NormProblem& p, hipStream_t stream);
 
 // A whole layer for at most 16 tokens (few.hip).
 constexpr int kFewW16 = 0, kFewFp8 = 1, kFewMx = 2;
-constexpr int kFewPartCols = 512 * 64;   // parts x columns of the down kernel at most
+constexpr int kFewPartCols = 512 * 128;   // parts x columns of the down kernel at most
 struct FewProblem {
   const void* x;            // [T, H] of dtype (kF16 / kBF16)
   const float* w_router;    // [E, H], or nullptr: ids and weights are given

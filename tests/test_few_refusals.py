@@ -40,7 +40,7 @@ def test_scales_and_block_rows():
 
 def test_workspace_bytes():
     f = _lib.lib().moe_few_workspace_bytes
-    assert f(16, 8, 256, 2048) == 16 * 256 * 4 + 16 * 8 * 2048 * 4 + 16 * 32768 * 4   # logits, hidden, parts of y
+    assert f(16, 8, 256, 2048) == 16 * 256 * 4 + 16 * 8 * 2048 * 4 + 16 * 65536 * 4   # logits, hidden, parts of y
     assert f(17, 8, 256, 2048) == 0 and f(1, 8, 256, 100) == 0 and f(1, 0, 256, 128) == 0
     n = f(4, 2, 8, 256)
     assert _few(ws_bytes=n - 1) == WORKSPACE
