@@ -100,14 +100,22 @@ __global__ __launch_bounds__(kMaxThreads) void block_norm_kernel(NormProblem a) 
   const int64_t base = t * a.H;
   const float inv_h = 1.0f / static_cast<float>(a.H);
 
+  // Columns past H: their loads go to the row's last vector, their values are
+  // zeros (a select where they enter r, nothing is computed around branches).
   int col[NV];
+  bool live[NV];
   float v[NV][V], r[NV][V];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     col[i] = (i * threads + tid) * V;
+    live[i] = col[i] < a.H;
+    col[i] = live[i] ? col[i] : a.H - V;
+    load_vals<RDT, V>(a.res, base + col[i], r[i]);
 #pragma unroll
-    for (int j = 0; j < V; ++j) v[i][j] = r[i][j] = 0.0f;
-    if (col[i] < a.H) load_vals<RDT, V>(a.res, base + col[i], r[i]);
+    for (int j = 0; j < V; ++j) {
+      r[i][j] = live[i] ? r[i][j] : 0.0f;
+      v[i][j] = 0.0f;
+    }
   }
 
   if (REDUCE || a.y) {
@@ -117,7 +125,6 @@ __global__ __launch_bounds__(kMaxThreads) void block_norm_kernel(NormProblem a) 
       for (int k0 = 0; k0 < a.K; k0 += kSlots) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          if (col[i] >= a.H) continue;
           float f[kSlots][V];
           int32_t p[kSlots];
 #pragma unroll
@@ -138,7 +145,7 @@ __global__ __launch_bounds__(kMaxThreads) void block_norm_kernel(NormProblem a) 
     } else {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        if (col[i] < a.H) load_vals<DT, V>(a.y, base + col[i], v[i]);
+        load_vals<DT, V>(a.y, base + col[i], v[i]);
       }
     }
 
@@ -148,7 +155,7 @@ __global__ __launch_bounds__(kMaxThreads) void block_norm_kernel(NormProblem a) 
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) ss = __builtin_fmaf(v[i][j], v[i][j], ss);
+        for (int j = 0; j < V; ++j) ss = live[i] ? __builtin_fmaf(v[i][j], v[i][j], ss) : ss;
       }
       ss = block_reduce<false>(ss, part[0], waves);
       rstd = 1.0f / sqrtf(ss * inv_h + a.eps);
@@ -157,7 +164,6 @@ __global__ __launch_bounds__(kMaxThreads) void block_norm_kernel(NormProblem a) 
     if (a.gate_kind == MOE_GATE_TOKEN) scale *= static_cast<const float*>(a.gate)[t];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (col[i] >= a.H) continue;
       float g[V];
       if (a.gamma_post) {
         load_vals<kF32, V>(a.gamma_post, col[i], g);
@@ -174,8 +180,8 @@ __global__ __launch_bounds__(kMaxThreads) void block_norm_kernel(NormProblem a) 
         for (int j = 0; j < V; ++j) v[i][j] *= g[j];
       }
 #pragma unroll
-      for (int j = 0; j < V; ++j) r[i][j] = __builtin_fmaf(scale, v[i][j], r[i][j]);
-      if (a.res_out) store_vals<RDT, V>(a.res_out, base + col[i], r[i]);
+      for (int j = 0; j < V; ++j) r[i][j] = live[i] ? __builtin_fmaf(scale, v[i][j], r[i][j]) : 0.0f;
+      if (a.res_out && live[i]) store_vals<RDT, V>(a.res_out, base + col[i], r[i]);
     }
   }
   if (!a.gamma_pre) return;
@@ -184,22 +190,21 @@ __global__ __launch_bounds__(kMaxThreads) void block_norm_kernel(NormProblem a) 
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) ss = __builtin_fmaf(r[i][j], r[i][j], ss);   // lanes past H hold zeros
+    for (int j = 0; j < V; ++j) ss = __builtin_fmaf(r[i][j], r[i][j], ss);   // zeros past H
   }
   ss = block_reduce<false>(ss, part[1], waves);
   const float rstd = 1.0f / sqrtf(ss * inv_h + a.eps);
   float amax = 0.0f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    if (col[i] >= a.H) continue;
     float g[V];
     load_vals<kF32, V>(a.gamma_pre, col[i], g);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      r[i][j] = r[i][j] * rstd * g[j];
+      r[i][j] = live[i] ? r[i][j] * rstd * g[j] : 0.0f;
       amax = fmaxf(amax, fabsf(r[i][j]));
     }
-    if (a.h) store_vals<DT, V>(a.h, base + col[i], r[i]);
+    if (a.h && live[i]) store_vals<DT, V>(a.h, base + col[i], r[i]);
   }
   if (a.quant == MOE_QUANT_NONE) return;
 
@@ -212,7 +217,6 @@ __global__ __launch_bounds__(kMaxThreads) void block_norm_kernel(NormProblem a) 
     uint8_t* out = static_cast<uint8_t*>(a.codes) + base;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (col[i] >= a.H) continue;
       uint32_t q[(V + 3) / 4] = {};
       if (fp8) {
         if constexpr (V == 8) {
@@ -230,6 +234,7 @@ __global__ __launch_bounds__(kMaxThreads) void block_norm_kernel(NormProblem a) 
           q[j >> 2] |= (static_cast<uint32_t>(static_cast<int>(c)) & 0xffu) << (8 * (j & 3));
         }
       }
+      if (!live[i]) continue;
       if constexpr (V == 8) *reinterpret_cast<u32x2*>(out + col[i]) = u32x2{q[0], q[1]};
       else out[col[i]] = static_cast<uint8_t>(q[0]);
     }
@@ -247,7 +252,7 @@ __global__ __launch_bounds__(kMaxThreads) void block_norm_kernel(NormProblem a) 
       for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(r[i][j]));
       m = fmaxf(m, __shfl_xor(m, 1));
       m = fmaxf(m, __shfl_xor(m, 2));
-      if (col[i] >= a.H) continue;
+      if (!live[i]) continue;
       const int e = mx_scale_exp(m, fp4 ? 2 : 8);
       if ((tid & 3) == 0) static_cast<uint8_t*>(a.scales)[t * nb + col[i] / 32] = static_cast<uint8_t>(e);
       const float X = ldexpf(1.0f, e - 127);
@@ -277,6 +282,10 @@ hipError_t launch_nv(const NormProblem& a, hipStream_t stream) {
 
 template <int DT, int RDT>
 hipError_t launch_typed(const NormProblem& a, hipStream_t stream) {
+  // single values: as many threads as a workgroup holds (bf16, graph of twenty
+  // calls: T = 900, H = 7001 23.0 us; T = 300, H = 16383 23.9 us; one row of 7001 6.6 us)
+  if (!a.vec && a.H <= 2 * kMaxThreads) return launch_nv<DT, RDT, 1, 2>(a, stream);
+  if (!a.vec && a.H <= 8 * kMaxThreads) return launch_nv<DT, RDT, 1, 8>(a, stream);
   if (!a.vec) return launch_nv<DT, RDT, 1, 16>(a, stream);     // up to 16384 values
   // Two vectors a thread where rows are long and there are more of them than
   // CUs: more, smaller workgroups then overlap their reductions' waits. H =
