@@ -554,7 +554,7 @@ moe_status moe_reduce_fused_scaled(const void* expert_out, int64_t rows,
  *                (codes [T, H] / [T, H/2], E8M0 scales [T, H/32]); the
  *                definitions of moe_quantize_fp8_rows, _int8_rows and _mx_rows
  *                with n in fp32 (not rounded to dtype first).
- * dtype: MOE_F16, MOE_BF16 or MOE_F32. Requires T >= 0, 1 <= H <= 16384,
+ * dtype: MOE_F16, MOE_BF16 or MOE_F32. Requires 0 <= T < 2^22, 1 <= H <= 16384,
  * eps > 0; the MX forms need H % 32 == 0 and y, residual, residual_out, h,
  * codes, the gammas and the gate on 16-byte boundaries. Other buffers must
  * not overlap. Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE,
@@ -608,8 +608,8 @@ moe_status moe_reduce_norm(const void* expert_out, int64_t rows,
  *   workspace: moe_few_workspace_bytes, 256-byte aligned; it holds the logits
  *   [T, E] at offset 0 and is written by every call (calls that overlap on
  *   two streams need one each).
- * Requires H % 256 == 0, D % 128 == 0 (_mx: D % 256 == 0), 1 <= E <= 1024,
- * 1 <= K <= 64 (and K <= E with w_router); x, y, w_router, weights and
+ * Requires H % 256 == 0, D % 128 == 0 (_mx: D % 256 == 0), H and D <= 2^24,
+ * T * K * D <= 2^28, 1 <= E <= 1024, 1 <= K <= 64 (and K <= E with w_router); x, y, w_router, weights and
  * MXFP4 scales on 16-byte boundaries. T == 0 returns MOE_OK and launches nothing.
  * Three kernels (four with w_router), no atomics on memory: results do not
  * depend on the run. Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE,

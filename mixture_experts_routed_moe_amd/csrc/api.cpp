@@ -981,8 +981,8 @@ static moe_status run_few(moe::FewProblem& p, void* workspace, size_t workspace_
     return fail(MOE_ERR_SHAPE, "MXFP4 weights need D a multiple of 256 (got %d)", p.D);
   }
   // lane offsets are 32 bits: 16 rows of x or of a weight, the hidden rows
-  if (p.H > (1 << 24) || static_cast<int64_t>(p.T) * p.K * p.D > (int64_t{1} << 28)) {
-    return fail(MOE_ERR_SHAPE, "H or T * K * D too large");
+  if (p.H > (1 << 24) || p.D > (1 << 24) || static_cast<int64_t>(p.T) * p.K * p.D > (int64_t{1} << 28)) {
+    return fail(MOE_ERR_SHAPE, "H, D or T * K * D too large");
   }
   if (!is_16bit(p.dtype)) return fail(MOE_ERR_DTYPE, "dtype must be MOE_F16 or MOE_BF16");
   uintptr_t bits = 0;

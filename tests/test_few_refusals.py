@@ -48,3 +48,9 @@ def test_workspace_bytes():
 
 def test_no_tokens_launch_nothing():
     assert _few(T=0) == 0 and _few("_mx", T=0, router=None) == 0
+
+
+def test_hidden_dimension_past_32_bit_offsets():
+    """16 rows of a down weight have to lie within a lane's 32-bit offset."""
+    assert _few(T=1, K=1, D=(1 << 24) + 256) == SHAPE
+    assert _few("_mx", T=1, K=1, D=1 << 25) == SHAPE
