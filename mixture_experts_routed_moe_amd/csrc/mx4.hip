@@ -264,6 +264,7 @@ template <int DT, bool GATEUP, int NBMAX, int NW, int TILES, int S, int WAVES>
 __global__ __launch_bounds__(64 * NW, WAVES) void mx4_grouped_kernel(Mx4Args g) {
   using SH = Mx4Shape<NW, TILES, NBMAX>;
   constexpr int H = TILES / 2;
+  static_assert(H == 2, "a wave's gate and up tiles cover one 32-column block");
   __shared__ __attribute__((aligned(16))) Mx4Lds<SH> lds;
   const int total = g.active_count[0] * g.n_tiles;
   const int per_xcd = (total + 7) >> 3;
@@ -326,10 +327,11 @@ __global__ __launch_bounds__(64 * NW, WAVES) void mx4_grouped_kernel(Mx4Args g) 
       constexpr int nb = decltype(NBC)::value;
       mx4_pass<nb, SH, TILES, S>(walk, w_off, s_off, static_cast<int>(16 * kb), a_off, as_off, np, tid, lr, lg, lds, acc);
       if constexpr (GATEUP) {
-        // The hidden values take the gate's registers; amax over the 4 lanes of a row. TILES = 2: a
-        // 32-column block is two waves' (w, w ^ 1), which exchange their maxima through LDS.
-        float* part = reinterpret_cast<float*>(&lds.row[0][0][0]);   // [NW][16 NBMAX], every read of the pass is done
-        auto hidden = [&](int q) __attribute__((always_inline)) {
+        // The hidden values take the gate's registers; a 32-column block is the wave's two tiles of a
+        // row, its amax over the row's 4 lanes.
+#pragma unroll
+        for (int q = 0; q < nb; ++q) {
+          const int row = 16 * q + lr;
           float amax = 0.0f;
 #pragma unroll
           for (int t = 0; t < H; ++t) {
@@ -340,38 +342,20 @@ __global__ __launch_bounds__(64 * NW, WAVES) void mx4_grouped_kernel(Mx4Args g) 
             }
           }
           amax = fmaxf(amax, __shfl_xor(amax, 16));
-          return fmaxf(amax, __shfl_xor(amax, 32));
-        };
-        if constexpr (H == 1) {
-#pragma unroll
-          for (int q = 0; q < nb; ++q) {
-            const float amax = hidden(q);
-            if (lg == 0) part[wave * (16 * NBMAX) + 16 * q + lr] = amax;
-          }
-          __syncthreads();
-        }
-#pragma unroll
-        for (int q = 0; q < nb; ++q) {
-          const int row = 16 * q + lr;
-          const float amax = H == 2 ? hidden(q)
-                                    : fmaxf(part[wave * (16 * NBMAX) + row], part[(wave ^ 1) * (16 * NBMAX) + row]);
+          amax = fmaxf(amax, __shfl_xor(amax, 32));
           const int e8 = mx_scale_exp(amax, 2);
           const float X = ldexpf(1.0f, e8 - 127);
           float v[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = i < 4 * H ? acc[q][i >> 2][i & 3] : 0.0f;
+          for (int i = 0; i < 8; ++i) v[i] = acc[q][i >> 2][i & 3];
           const uint32_t q0 = pk8_fp4e2m1(v, X);           // 16 bits a tile
           const uint32_t q1 = __shfl_xor(q0, 16), q2 = __shfl_xor(q0, 32), q3 = __shfl_xor(q0, 48);
           if (row < rows_pass && lg == 0) {     // lane group 0 collects the row: q1, q2, q3 are groups 1, 2, 3
             const int64_t at = m_start + r0 + row;
             uint8_t* codes = g.hq + at * (g.n / 2) + col0 / 2;
             const uint32_t c0 = (q0 & 0xffffu) | (q1 << 16), c1 = (q2 & 0xffffu) | (q3 << 16);
-            if constexpr (H == 1) {
-              *reinterpret_cast<u32x2*>(codes) = u32x2{c0, c1};
-            } else {
-              *reinterpret_cast<u32x4*>(codes) = u32x4{c0, c1, (q0 >> 16) | (q1 & 0xffff0000u), (q2 >> 16) | (q3 & 0xffff0000u)};
-            }
-            if (H == 2 || (wave & 1) == 0) g.hs[at * (g.n / kBlk) + col0 / kBlk] = static_cast<uint8_t>(e8);
+            *reinterpret_cast<u32x4*>(codes) = u32x4{c0, c1, (q0 >> 16) | (q1 & 0xffff0000u), (q2 >> 16) | (q3 & 0xffff0000u)};
+            g.hs[at * (g.n / kBlk) + col0 / kBlk] = static_cast<uint8_t>(e8);
           }
         }
       } else {
