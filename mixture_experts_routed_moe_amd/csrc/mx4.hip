@@ -21,13 +21,13 @@
 // another. (With the 32x32x64 instruction a load reads 16-byte pieces of 32
 // lines and each line is asked for four times; the first-level cache stalls on
 // a line that is still on its way: T = 4096 gate/up 1376 us, T = 512 890 us
-// against 953 and 694 here.)
+// against 938 and 679 here.)
 //
 // Scales: a row's bytes are loaded 64 at a time (eight pairs of chunks), go
 // through LDS, and a lane moves its byte of each 4 down by a shift. Rows of
 // scales are short strips of lines that the first-level cache does not keep
 // between two pairs: loaded 8 or 16 bytes at a time they cost T = 512 gate/up
-// 818 or 737 us, against 694 us here.
+// 818 or 737 us, against 694 us so (679 with the single buffer below).
 //
 // Bound: the weight stream (a prefill expert of ~128 rows needs 8 x 16 cycles
 // of MFMA a 1 KB weight load, a third of the time HBM takes to deliver it).
@@ -103,6 +103,13 @@ struct Mx4Shape {
   static constexpr int scale_loads(int nb) { return (16 * nb + kThreads / 4 - 1) / (kThreads / 4); }
   static constexpr int kScaleRows = scale_loads(NBMAX) * (kThreads / 4);
   static constexpr int kWeightRows = kThreads / 64 * 16 * TILES;
+  // A wave alone writes and reads its weights' scales, so one buffer of them is
+  // enough and lighter on LDS (two -> one: T = 512 697 + 418 -> 679 + 411 us,
+  // T = 1024 in blocks of 64 723 + 441 -> 715 + 436). Two leave the compiler more
+  // room between a strip's writes and its reads, which tall passes need (T =
+  // 4096: 938 + 613 us, with one 1088 + 734) and single groups gain a little
+  // from (128 x 2048 x 768, T = 67: gate/up 42.8, 43.7 us).
+  static constexpr int kWeightBufs = NBMAX == 1 || NBMAX >= 8 ? 2 : 1;
 };
 
 template <int NS, int TILES>
@@ -115,7 +122,7 @@ template <typename SH>
 struct Mx4Lds {
   uint8_t row[2][SH::kRows][kLdsRow];
   uint8_t as[2][SH::kScaleRows][kScaleRow];    // scales of the activation rows
-  uint8_t ws[2][SH::kWeightRows][kScaleRow];   // and of every wave's weight rows
+  uint8_t ws[SH::kWeightBufs][SH::kWeightRows][kScaleRow];   // and of every wave's weight rows
 };
 
 // Where a pass reads: wave-uniform addresses that walk along the reduction, and
@@ -179,7 +186,7 @@ __device__ __forceinline__ void mx4_pass(Mx4Walk<TILES> p, uint32_t w_off, uint3
     }
 #pragma unroll
     for (int t = 0; t < TILES; ++t) {
-      *reinterpret_cast<u32x4*>(&lds.ws[buf][(wave * TILES + t) * 16 + lr][lg * 16]) = sw_next[t];
+      *reinterpret_cast<u32x4*>(&lds.ws[buf % SH::kWeightBufs][(wave * TILES + t) * 16 + lr][lg * 16]) = sw_next[t];
     }
   };
   auto stage = [&](const Mx4Slot<NS, TILES>& s, int buf) __attribute__((always_inline)) {
@@ -218,7 +225,7 @@ __device__ __forceinline__ void mx4_pass(Mx4Walk<TILES> p, uint32_t w_off, uint3
     uint32_t wa[2][TILES];
 #pragma unroll
     for (int t = 0; t < TILES; ++t) {
-      const u32x2 sw = *reinterpret_cast<const u32x2*>(&lds.ws[g][(wave * TILES + t) * 16 + lr][V * kPairScales]);
+      const u32x2 sw = *reinterpret_cast<const u32x2*>(&lds.ws[g % SH::kWeightBufs][(wave * TILES + t) * 16 + lr][V * kPairScales]);
       wa[0][t] = sw.x >> (8 * lg);
       wa[1][t] = sw.y >> (8 * lg);
     }
