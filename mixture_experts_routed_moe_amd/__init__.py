@@ -11,6 +11,7 @@ MoeError with the library's status code on any failure.
     y = moe_routed_forward(x, w_gate, w_up, w_down, tables)         # steps 2-3
     y = moe_reduce_fused(expert_out, token_topk_to_pos, topk_weights)  # step 3 alone
     residual, h = moe_block_norm(y, residual, gamma_post, gamma_pre)   # the norms between blocks
+    y, ids, weights = moe_layer_few(x, w_router, w_gate, w_up, w_down, top_k)   # steps 0-3, T <= 16
 """
 import ctypes
 import math
