@@ -125,6 +125,28 @@ def test_reduce_fp32_against_float64(T, H, K):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_more_rows_than_a_grid_dimension_of_16_bits():
+    d = _inputs(70001, 64, "token", seed=5)
+    got_r, got_h = _call(d)
+    r, err_r, n, err_n = _reference(d)
+    assert ((got_r.double() - r).abs() <= err_r).all() and ((got_h.double() - n).abs() <= err_n).all()
+
+
+def test_combine_of_rows_off_the_vector_boundary():
+    """Bases off a 16-byte boundary: the same values as on it, one at a time."""
+    d = _inputs(9, 512, "channel", seed=6, K=4)
+    want = _call(d)
+    off = dict(d)
+    for k in ("rows", "residual"):
+        buf = torch.empty(d[k].numel() + 1, device=DEV)
+        off[k] = buf[1:].view(d[k].shape)
+        off[k].copy_(d[k])
+    got = _call(off)
+    r, err_r, n, err_n = _reference(d)
+    for g in (want, got):
+        assert ((g[0].double() - r).abs() <= err_r).all() and ((g[1].double() - n).abs() <= err_n).all()
+
+
 def _wide(d):
     """The same values in fp32."""
     return {k: v.float() if torch.is_tensor(v) and v.dtype.is_floating_point else v for k, v in d.items()}

@@ -250,6 +250,23 @@ def test_nothing_leaks_between_tokens_and_experts(kind):
     assert torch.equal(got[keep], clean[keep])
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("T, H, D, E, K", [(16, 256, 256, 1024, 64), (1, 65792, 256, 2, 1), (16, 65792, 256, 2, 2)])
+def test_every_expert_and_the_longest_rows(kind, T, H, D, E, K):
+    """1024 distinct experts in one call; more column tiles than workgroups run
+    at once (the down kernel then writes y itself)."""
+    mr = _mr()
+    g = _gen(T + E)
+    x = torch.randn(T, H, generator=g, device=DEV).to(torch.bfloat16)
+    (wg, vg), (wu, vu), (wd, vd) = (_random_weights(E, *s, kind, torch.bfloat16, g) for s in ((D, H), (D, H), (H, D)))
+    ids = torch.randperm(T * K, generator=g, device=DEV).view(T, K).to(torch.int32) % E
+    w = torch.rand(T, K, generator=g, device=DEV)
+    y = mr.moe_layer_few_routed(x, ids, w, wg, wu, wd)
+    torch.cuda.synchronize()
+    want, err = _layer64(x, ids, w, vg, vu, vd)
+    _close(y, want, err)
+
+
 def test_weights_none_and_all_masked():
     mr = _mr()
     T, H, D, E, K, dtype = 4, 256, 128, 6, 3, torch.float16
