@@ -39,6 +39,7 @@
 
 #include "common.hpp"
 #include "launch.hpp"
+#include "mx_codes.hpp"
 
 namespace moe {
 namespace {
